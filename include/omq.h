@@ -517,6 +517,155 @@ typedef struct {
 omq_status omq_block_calibrate(const omq_block_calib_args* args, void* workspace,
                                size_t ws_bytes, omq_stream_t stream);
 
+/* ====================================================================================
+ * The 4-bit paged key / value cache ([ICLR] section LET: Q, K and V are quantized "for a
+ * low-bit KV cache"; the page names no layout: pages, cells and the step's plan are ours).
+ * Between the folded q|k|v product (omq_qgemv / omq_qgemm) and the folded output projection
+ * a serving step runs
+ *   omq_kv_plan    pages, slots and positions of the step's new tokens, from the lengths
+ *   omq_kv_append  RoPE, LET scales and per-(token, head) 4-bit quantization into the slots
+ *   omq_kv_attn    softmax attention of the new tokens' queries over the cache
+ * and omq_kv_read gives the stored values back. Nothing here synchronises: all four take the
+ * requests' state from device memory, so a step can be captured in a graph and replayed.
+ *
+ * Pool: uint8 [n_pages, Hkv, page / 16, cell]. A cell is 16 consecutive tokens of one kv
+ * head, omq_kv_cell_bytes(D) = 16 D + 256 bytes back to back:
+ *   K codes [16, D/2] | V codes [16, D/2] | K h f32 [16] | K z i32 [16] | V h f32 [16] | V z i32 [16]
+ * element d of a row in byte d / 2, low nibble first (omq_fold_pack's rule). The stored value
+ * is (c - z) h. Token position t of request r lies in page table[r][t / page], at offset
+ * t mod page of it; its slot is page id * page + offset. page is a multiple of 16, at most
+ * 4096; D is 64 or 128; n_pages * page < 2^31. The pool's bytes need no initialisation: no
+ * result depends on a slot that no omq_kv_append wrote, unless a length says it is there.
+ * ==================================================================================== */
+typedef struct {
+  void* data;        /* [n_pages, Hkv, page / 16, cell], 16-byte aligned */
+  int64_t n_pages;
+  int64_t page;      /* tokens per page */
+  int64_t Hkv;       /* kv heads */
+  int64_t D;         /* head size */
+} omq_kv_pool;
+
+/* Bytes of a 16-token cell of one kv head (0 for a head size that is not supported). */
+size_t omq_kv_cell_bytes(int64_t D);
+
+/* The rotary table omq_kv_append takes: table [2, n_pos, D/2] float32, cos then sin of
+ * position * base^(-2i/D), in binary64 rounded once (the block's rotary rule). */
+omq_status omq_rope_table(int64_t n_pos, int64_t D, double base, float* table,
+                          omq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * omq_kv_plan — one step's bookkeeping on the device. Request b has lens[b] cached tokens in
+ * the first ceil(lens[b] / page) pages of table[b] and asks for new_tokens[b] more (0: none;
+ * negative: it is finished, its pages go back to the pool and its length becomes 0).
+ * free_pages[0 .. n_free) is a stack of free page ids. In request order,
+ *   - pages of finished requests are pushed (request by request, first page first; a stack
+ *     already holding n_pages ids takes no more);
+ *   - a request is refused (gets no tokens, keeps its length) when ceil((lens + new) / page)
+ *     > width, or when it needs pages and the needs up to and including its own exceed the
+ *     free pages, or when the tokens asked for up to and including its own (not counting
+ *     requests refused before) exceed `capacity`;
+ *   - the others take their new pages from the top of the stack into table[b][held ..].
+ * lens_out[b], n_free_out: the state after the step. They may be lens and n_free themselves
+ * (in place); given other arrays, the call may be repeated with the same result.
+ * cu [n_req + 1]: request b's granted tokens are rows cu[b] .. cu[b + 1] - 1 of the step.
+ * slots, positions, requests [capacity]: each row's slot, position and request, -1 behind
+ * the last row. Lengths outside 0 .. width * page count as the nearer bound.
+ * One launch; n_req up to 65536, width * page < 2^31.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  const int32_t* lens;         /* [n_req] */
+  const int32_t* new_tokens;   /* [n_req] */
+  int64_t n_req;
+  int32_t* table;              /* [n_req, width], new pages written in place */
+  int64_t width, page;
+  int32_t* free_pages;         /* [n_pages], pages given back written in place */
+  int64_t n_pages;
+  const int32_t* n_free;       /* [1] */
+  int32_t* lens_out;           /* [n_req] */
+  int32_t* n_free_out;         /* [1] */
+  int32_t* cu;                 /* [n_req + 1] */
+  int32_t* slots;              /* [capacity] */
+  int32_t* positions;          /* [capacity] */
+  int32_t* requests;           /* [capacity] */
+  int64_t capacity;            /* rows of the step, >= 1 */
+} omq_kv_plan_args;
+omq_status omq_kv_plan(const omq_kv_plan_args* args, omq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * omq_kv_append — T tokens' keys and values into the cache, and their queries made ready.
+ * Per row of D values, binary32, one rounding per operation (the order of omq_block_step):
+ *   k~ = RoPE(k) s_a, v~ = (v - delta_o) / s_o, q~ = RoPE(q) / s_a
+ *   h = max((max - min) / 15, 1e-8), z = -round(min / h), c = clamp(round(x / h) + z, 0, 15)
+ *   q_out = q~ in q_dt, or for abits < 16 its fake-quant with 2^abits - 1 in place of 15
+ * A row holding a NaN or an infinity, or whose range overflows, is stored with h = NaN and
+ * reads back as NaN. RoPE takes pairs (i, i + D/2) and row positions[t] of the table; no
+ * positions (or no table): no rotation. s_a, s_o, delta_o [Hkv, D] or NULL (no transform);
+ * query head j shares those of kv head j / (Hq / Hkv).
+ * q, k, v: [T, Hq or Hkv, D] in dt, a token's heads back to back, tokens q_ld / k_ld / v_ld
+ * elements apart (slices of one fused product are fine; rows 16-byte aligned). q may be NULL.
+ * q_out [T, Hq, D] dense. A token whose slot is outside the pool (-1 in particular) or whose
+ * position is outside the table is skipped: nothing stored, its row of q_out left as it was.
+ * Two rows with the same slot leave that slot with either row's values, or some of each.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  omq_kv_pool pool;
+  int64_t T, Hq;
+  omq_dtype dt;
+  const void* q; const void* k; const void* v;
+  int64_t q_ld, k_ld, v_ld;
+  const int32_t* slots;        /* [T] */
+  const int32_t* positions;    /* [T] or NULL */
+  const float* rope;           /* [2, n_pos, D/2] or NULL */
+  int64_t n_pos;
+  const float* s_a; const float* s_o; const float* delta_o;
+  int abits;                   /* of q: 2, 3, 4, 6, 8, or 16 (not quantized) */
+  void* q_out;
+  omq_dtype q_dt;
+} omq_kv_append_args;
+omq_status omq_kv_append(const omq_kv_append_args* args, omq_stream_t stream);
+
+/* omq_kv_read — the stored values (c - z) h of T slots: k, v [T, Hkv, D] dense in dt. A slot
+ * outside the pool reads as zeros. */
+omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots, void* k, void* v,
+                       omq_dtype dt, omq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * omq_kv_attn — softmax attention over the cache. Request b's queries are rows cu[b] ..
+ * cu[b + 1] - 1 of q, the last tokens of its lens[b] cached ones (their keys already stored):
+ *   o_i = sum_j p_ij v_j,  p_ij = softmax over j of scale q_i . k_j,  k_j, v_j = (c - z) h
+ * over j <= lens[b] - n_b + i (causal, i counted from the request's first row) or all
+ * j < lens[b]. Query head h reads kv head h / (Hq / Hkv). A position whose table entry is
+ * outside 0 .. n_pages - 1 holds no key. A row without a key gets zeros (lse -inf). Rows of
+ * q behind cu[n_req] are left as they were, as are a request's rows from max_q on.
+ * q [T, Hq, D] F16 or BF16, tokens q_ld elements apart, rows 16-byte aligned; out [T, Hq, D]
+ * dense, F16 or BF16; lse [T, Hq] float32 (natural log of the softmax's denominator) or NULL.
+ * The codes are exact operands and sums, statistics and steps are float32; the weights are
+ * rounded to float16 relative to the row's largest, q exactly unless an element is 2^-28 of
+ * its row's largest. Results are bitwise reproducible.
+ * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL).
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  omq_kv_pool pool;
+  int64_t n_req;
+  int64_t T, Hq;               /* Hq a multiple of Hkv */
+  const void* q;
+  int64_t q_ld;
+  omq_dtype dt;
+  const int32_t* table;        /* [n_req, width] */
+  int64_t width;
+  const int32_t* lens;         /* [n_req], the new tokens included */
+  const int32_t* cu;           /* [n_req + 1] */
+  int64_t max_q;               /* most rows of a request */
+  float scale;
+  int causal;
+  void* out;
+  omq_dtype out_dt;
+  float* lse;
+} omq_kv_attn_args;
+omq_status omq_kv_attn(const omq_kv_attn_args* args, void* workspace, size_t ws_bytes,
+                       omq_stream_t stream);
+size_t omq_kv_attn_workspace_bytes(const omq_kv_attn_args* args);
+
 /* Number of kernels this library has launched in this process (all threads, all devices),
  * counted on the host at each launch. */
 uint64_t omq_launch_count(void);

@@ -56,7 +56,8 @@ struct AttnPrepParams {
   float* part_do;
 };
 
-omq_status launch_rope_table(int64_t M, double base, float* cos_t, float* sin_t, cudaStream_t st);
+omq_status launch_rope_table(int64_t M, double base, float* cos_t, float* sin_t, cudaStream_t st,
+                             int half = 64);
 omq_status launch_rms(const RmsParams& p, cudaStream_t st);
 omq_status launch_rms_bwd(const RmsBwdParams& p, cudaStream_t st);
 omq_status launch_attn_prep(const AttnPrepParams& p, bool backward, cudaStream_t st);

@@ -530,8 +530,8 @@ static unsigned grid_for(int64_t work, int64_t per_block, int cap_per_sm) {
 }
 
 omq_status launch_rope_table(int64_t M, double base, float* cos_t, float* sin_t,
-                             cudaStream_t st) {
-  launch_k(rope_table_kernel, grid_for(M * 64, 256, 8), 256, 0, st, M, 64, base, cos_t, sin_t);
+                             cudaStream_t st, int half) {
+  launch_k(rope_table_kernel, grid_for(M * half, 256, 8), 256, 0, st, M, half, base, cos_t, sin_t);
   return launch_status();
 }
 

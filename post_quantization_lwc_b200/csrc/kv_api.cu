@@ -1,0 +1,168 @@
+// C entry points of the 4-bit paged key/value cache: validation on the host, then the launches.
+#include "block_internal.cuh"
+#include "kv_internal.cuh"
+
+namespace omq {
+namespace {
+
+constexpr int64_t kMaxPage = 4096, kMaxHeads = 65536, kMaxReq = 65536, kMaxLd = int64_t{1} << 31;
+
+bool any_float(omq_dtype d) { return d == OMQ_F32 || d == OMQ_BF16 || d == OMQ_F16; }
+bool sixteen(omq_dtype d) { return d == OMQ_BF16 || d == OMQ_F16; }
+int64_t esize(omq_dtype d) { return d == OMQ_F32 ? 4 : 2; }
+
+omq_status check_pool(const omq_kv_pool& p) {
+  if (!p.data) return OMQ_ERR_NULL;
+  if (p.D != 64 && p.D != 128) return OMQ_ERR_SHAPE;
+  if (p.page < 16 || p.page % 16 || p.page > kMaxPage) return OMQ_ERR_SHAPE;
+  if (p.n_pages < 1 || p.n_pages > (int64_t{1} << 31) / p.page - 1) return OMQ_ERR_SHAPE;
+  if (p.Hkv < 1 || p.Hkv > kMaxHeads) return OMQ_ERR_SHAPE;
+  if (!aligned16(p.data)) return OMQ_ERR_ALIGN;
+  return OMQ_OK;
+}
+kv::Pool view(const omq_kv_pool& p) {
+  return kv::Pool{static_cast<uint8_t*>(p.data), p.n_pages, static_cast<int>(p.Hkv),
+                  static_cast<int>(p.page / 16), static_cast<int>(p.page)};
+}
+// Rows of `heads` heads, `ld` elements apart, each 16-byte aligned.
+omq_status check_rows(const void* p, int64_t ld, int64_t heads, int64_t D, omq_dtype dt) {
+  if (!p) return OMQ_ERR_NULL;
+  if (ld < heads * D || ld > kMaxLd) return OMQ_ERR_SHAPE;
+  if (!aligned16(p) || (ld * esize(dt)) % 16) return OMQ_ERR_ALIGN;
+  return OMQ_OK;
+}
+
+#define KV_TRY(expr)                  \
+  do {                                \
+    omq_status _s = (expr);           \
+    if (_s != OMQ_OK) return _s;      \
+  } while (0)
+
+omq_status check_attn(const omq_kv_attn_args* a) {
+  if (!a) return OMQ_ERR_NULL;
+  KV_TRY(check_pool(a->pool));
+  if (!a->q || !a->table || !a->lens || !a->cu || !a->out) return OMQ_ERR_NULL;
+  if (!sixteen(a->dt) || !sixteen(a->out_dt)) return OMQ_ERR_DTYPE;
+  if (a->n_req < 1 || a->n_req > kMaxReq || a->T < 1 || a->T >= (int64_t{1} << 31)) return OMQ_ERR_SHAPE;
+  if (a->Hq < 1 || a->Hq > kMaxHeads || a->Hq % a->pool.Hkv) return OMQ_ERR_SHAPE;
+  if (a->width < 1 || a->width * a->pool.page >= (int64_t{1} << 31)) return OMQ_ERR_SHAPE;
+  if (a->max_q < 1 || a->max_q > a->T) return OMQ_ERR_SHAPE;
+  // a request's query rows per kv head, and the launch's blocks, stay 32-bit
+  const int64_t rows = a->max_q * (a->Hq / a->pool.Hkv);
+  if (rows >= (int64_t{1} << 30)) return OMQ_ERR_SHAPE;
+  if ((rows / 8 + 1) * a->pool.Hkv >= (int64_t{1} << 27) / a->n_req) return OMQ_ERR_SHAPE;
+  KV_TRY(check_rows(a->q, a->q_ld, a->Hq, a->pool.D, a->dt));
+  if (!aligned16(a->out)) return OMQ_ERR_ALIGN;
+  return OMQ_OK;
+}
+
+}  // namespace
+}  // namespace omq
+
+using namespace omq;
+
+extern "C" {
+
+size_t omq_kv_cell_bytes(int64_t D) {
+  return D == 64 || D == 128 ? static_cast<size_t>(kv::cell_bytes(D)) : 0;
+}
+
+omq_status omq_rope_table(int64_t n_pos, int64_t D, double base, float* table,
+                          omq_stream_t stream) {
+  if (!table) return OMQ_ERR_NULL;
+  if (n_pos < 1 || n_pos > (int64_t{1} << 24) || (D != 64 && D != 128) || !(base > 1.0))
+    return OMQ_ERR_SHAPE;
+  if (!aligned16(table)) return OMQ_ERR_ALIGN;
+  return launch_rope_table(n_pos, base, table, table + n_pos * (D / 2),
+                           reinterpret_cast<cudaStream_t>(stream), static_cast<int>(D / 2));
+}
+
+omq_status omq_kv_plan(const omq_kv_plan_args* a, omq_stream_t stream) {
+  if (!a || !a->lens || !a->new_tokens || !a->table || !a->free_pages || !a->n_free ||
+      !a->lens_out || !a->n_free_out || !a->cu || !a->slots || !a->positions || !a->requests)
+    return OMQ_ERR_NULL;
+  if (a->n_req < 1 || a->n_req > kMaxReq || a->capacity < 1 || a->capacity >= (int64_t{1} << 31))
+    return OMQ_ERR_SHAPE;
+  if (a->page < 16 || a->page % 16 || a->page > kMaxPage) return OMQ_ERR_SHAPE;
+  if (a->width < 1 || a->width >= (int64_t{1} << 31) / a->page) return OMQ_ERR_SHAPE;
+  if (a->n_pages < 1 || a->n_pages > (int64_t{1} << 31) / a->page - 1) return OMQ_ERR_SHAPE;
+  kv::PlanParams p{a->lens, a->new_tokens, static_cast<int>(a->n_req), a->table,
+                   static_cast<int>(a->width), static_cast<int>(a->page), a->free_pages,
+                   static_cast<int>(a->n_pages), a->n_free, a->lens_out, a->n_free_out, a->cu,
+                   a->slots, a->positions, a->requests, static_cast<int>(a->capacity)};
+  return kv::launch_plan(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+omq_status omq_kv_append(const omq_kv_append_args* a, omq_stream_t stream) {
+  if (!a) return OMQ_ERR_NULL;
+  KV_TRY(check_pool(a->pool));
+  if (!a->slots || !a->k || !a->v) return OMQ_ERR_NULL;
+  if (!any_float(a->dt)) return OMQ_ERR_DTYPE;
+  if (a->T < 1 || a->T >= (int64_t{1} << 31)) return OMQ_ERR_SHAPE;
+  const bool rot = a->rope && a->positions;
+  if (a->rope && (a->n_pos < 1 || a->n_pos >= (int64_t{1} << 31))) return OMQ_ERR_SHAPE;
+  if (!aligned16(a->rope) || !aligned16(a->s_a) || !aligned16(a->s_o) || !aligned16(a->delta_o))
+    return OMQ_ERR_ALIGN;
+  if (a->delta_o && !a->s_o) return OMQ_ERR_NULL;
+  KV_TRY(check_rows(a->k, a->k_ld, a->pool.Hkv, a->pool.D, a->dt));
+  KV_TRY(check_rows(a->v, a->v_ld, a->pool.Hkv, a->pool.D, a->dt));
+  const int ab = a->abits;
+  if (a->q) {
+    if (!a->q_out) return OMQ_ERR_NULL;
+    if (!any_float(a->q_dt)) return OMQ_ERR_DTYPE;
+    if (ab != 2 && ab != 3 && ab != 4 && ab != 6 && ab != 8 && ab != 16) return OMQ_ERR_BITS;
+    if (a->Hq < 1 || a->Hq > kMaxHeads || a->Hq % a->pool.Hkv) return OMQ_ERR_SHAPE;
+    KV_TRY(check_rows(a->q, a->q_ld, a->Hq, a->pool.D, a->dt));
+    if (!aligned16(a->q_out)) return OMQ_ERR_ALIGN;
+  }
+  const int64_t rows = (a->q ? a->Hq : 0) + 2 * a->pool.Hkv;
+  if (a->T > (int64_t{1} << 31) / rows) return OMQ_ERR_SHAPE;
+  kv::AppendParams p{};
+  p.pool = view(a->pool);
+  p.T = a->T;
+  p.Hq = a->q ? static_cast<int>(a->Hq) : 0;
+  p.q = a->q; p.k = a->k; p.v = a->v;
+  p.q_ld = a->q_ld; p.k_ld = a->k_ld; p.v_ld = a->v_ld;
+  p.dt = a->dt;
+  p.slots = a->slots;
+  p.positions = rot ? a->positions : nullptr;
+  p.rope = rot ? a->rope : nullptr;
+  p.n_pos = a->n_pos;
+  p.s_a = a->s_a; p.s_o = a->s_o; p.delta_o = a->delta_o;
+  p.quant_q = a->q && ab < 16;
+  p.Qa = static_cast<float>((1 << (p.quant_q ? ab : 1)) - 1);
+  p.q_out = a->q_out;
+  p.q_dt = a->q_dt;
+  return kv::launch_append(p, a->pool.D, reinterpret_cast<cudaStream_t>(stream));
+}
+
+omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots, void* k, void* v,
+                       omq_dtype dt, omq_stream_t stream) {
+  if (!pool) return OMQ_ERR_NULL;
+  KV_TRY(check_pool(*pool));
+  if (!slots || !k || !v) return OMQ_ERR_NULL;
+  if (!any_float(dt)) return OMQ_ERR_DTYPE;
+  if (T < 1 || T > (int64_t{1} << 31) / pool->Hkv) return OMQ_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v)) return OMQ_ERR_ALIGN;
+  kv::ReadParams p{view(*pool), T, slots, k, v, dt};
+  return kv::launch_read(p, pool->D, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t omq_kv_attn_workspace_bytes(const omq_kv_attn_args* a) {
+  (void)a;
+  return 0;
+}
+
+omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_bytes,
+                       omq_stream_t stream) {
+  KV_TRY(check_attn(a));
+  (void)workspace;
+  (void)ws_bytes;
+  kv::AttnParams p{view(a->pool), static_cast<int>(a->n_req), a->T, static_cast<int>(a->Hq),
+                   static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
+                   static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
+                   a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
+  return kv::launch_attn_rows(p, a->pool.D, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,185 @@
+// The plan of a serving step over the paged cache: pages back from finished requests, pages
+// for new tokens, and the slot, position and request of every new token, from the requests'
+// lengths, in one launch and without the host seeing any of them.
+//
+// With held = ceil(len / page) and need = ceil((len + n) / page) - held, everything is a prefix
+// sum over the requests: of the pages given back (their place on the free stack), of need (who
+// still gets pages, and which), and of n (who still fits the token capacity, and where a
+// request's tokens start). Block 0 of the launch's one cluster takes the requests in chunks
+// of its 512 threads; the cluster's barrier then publishes the lengths, the table and the token
+// offsets, and all its blocks write the token maps, each token finding its request by
+// bisection over the offsets in shared memory. A few microseconds of dependent loads and
+// barriers, whatever the size; bandwidth plays no part below some hundred thousand tokens.
+#include "kv_internal.cuh"
+
+namespace omq {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kCuShared = 4096;     // offsets kept in shared memory (more: read through L2)
+
+// Inclusive prefix sum over the block; *total receives the block's sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sm, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) sm[w] = v;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    const int64_t s = sm[i];
+    before += i < w ? s : 0;
+    all += s;
+  }
+  *total = all;
+  return v + before;
+}
+
+struct Req {
+  int64_t len, n, held, need;
+  bool release;
+};
+__device__ __forceinline__ Req load_req(const PlanParams& p, int b) {
+  Req r{0, 0, 0, 0, false};
+  if (b >= p.n_req) return r;
+  const int64_t room = static_cast<int64_t>(p.width) * p.page;
+  const int64_t len = p.lens[b];
+  const int64_t n = p.new_tokens[b];
+  r.len = len < 0 ? 0 : len > room ? room : len;
+  r.release = n < 0;
+  r.held = (static_cast<uint32_t>(r.len) + p.page - 1u) / static_cast<uint32_t>(p.page);
+  // refused where the table has no room for it
+  r.n = n > 0 && r.len + n <= room ? n : 0;
+  r.need = r.n ? (static_cast<uint32_t>(r.len + r.n) + p.page - 1u) / static_cast<uint32_t>(p.page) -
+                     r.held
+               : 0;
+  return r;
+}
+
+// The last i in [0, n) with off[i] <= t (off[0] = 0 <= t).
+template <class T>
+__device__ __forceinline__ int last_at_most(const T* off, int n, T t) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_plan_kernel(PlanParams p) {
+  pdl_wait();
+  pdl_launch();
+  __shared__ int64_t scan_sm[kThreads / 32];
+  __shared__ int32_t start[kThreads];        // a chunk's exclusive page prefix
+  __shared__ int32_t held_sm[kThreads];
+  __shared__ int32_t cu_sm[kCuShared + 1];
+  const int tid = threadIdx.x;
+  if (cta_rank() == 0) {
+    const int64_t free0 = min(max(*p.n_free, 0), p.n_pages);
+    // pages of released requests, in request order, onto the stack
+    int64_t back = 0;
+    for (int c = 0; c < p.n_req; c += kThreads) {
+      const int b = c + tid;
+      const Req r = load_req(p, b);
+      const int64_t cnt = r.release ? r.held : 0;
+      int64_t total;
+      const int64_t incl = block_scan(cnt, scan_sm, &total);
+      if (total) {                                        // block-uniform
+        start[tid] = static_cast<int32_t>(incl - cnt);
+        __syncthreads();
+        for (int64_t i = tid; i < total; i += kThreads) {
+          const int j = last_at_most(start, kThreads, static_cast<int32_t>(i));
+          const int64_t to = free0 + back + i;
+          if (to < p.n_pages)
+            p.free_pages[to] = p.table[static_cast<int64_t>(c + j) * p.width + (i - start[j])];
+        }
+        back += total;
+        __syncthreads();
+      }
+    }
+    const int64_t avail = min(free0 + back, static_cast<int64_t>(p.n_pages));
+    int64_t asked = 0, tokens = 0, given = 0, popped = 0;
+    for (int c = 0; c < p.n_req; c += kThreads) {
+      const int b = c + tid;
+      const Req r = load_req(p, b);
+      int64_t total;
+      const int64_t pages_in = asked + block_scan(r.need, scan_sm, &total);
+      asked += total;
+      const bool fits = r.need == 0 || pages_in <= avail;
+      const int64_t n1 = fits ? r.n : 0;
+      const int64_t tok_in = tokens + block_scan(n1, scan_sm, &total);
+      tokens += total;
+      const bool ok = fits && (n1 == 0 || tok_in <= p.capacity);
+      const int64_t n = ok ? n1 : 0;
+      const int64_t need = ok ? r.need : 0;
+      const int64_t cu_in = given + block_scan(n, scan_sm, &total);
+      given += total;
+      const int64_t pop_in = popped + block_scan(need, scan_sm, &total);
+      start[tid] = static_cast<int32_t>(pop_in - need - popped);
+      held_sm[tid] = static_cast<int32_t>(r.held);
+      __syncthreads();
+      // the pages granted in this chunk, from the top of the stack down
+      for (int64_t i = tid; i < total; i += kThreads) {
+        const int j = last_at_most(start, kThreads, static_cast<int32_t>(i));
+        p.table[static_cast<int64_t>(c + j) * p.width + held_sm[j] + (i - start[j])] =
+            p.free_pages[avail - 1 - (popped + i)];
+      }
+      popped += total;
+      if (b < p.n_req) {
+        p.lens_out[b] = static_cast<int32_t>(r.release ? 0 : r.len + n);
+        p.cu[b + 1] = static_cast<int32_t>(cu_in);
+      }
+      __syncthreads();
+    }
+    if (tid == 0) {
+      p.cu[0] = 0;
+      *p.n_free_out = static_cast<int32_t>(avail - popped);
+    }
+  }
+  // lengths, offsets and table are visible to the whole cluster after this
+  cluster_sync_all();
+  const int32_t* cu = p.cu;
+  const bool in_sm = p.n_req <= kCuShared;
+  if (in_sm)
+    for (int i = tid; i <= p.n_req; i += kThreads) cu_sm[i] = __ldcg(p.cu + i);
+  __syncthreads();
+  const int used = __ldcg(p.cu + p.n_req);
+  const int step = static_cast<int>(cta_count()) * kThreads;
+  for (int64_t t = static_cast<int64_t>(cta_rank()) * kThreads + tid; t < p.capacity; t += step) {
+    int slot = -1, pos = -1, req = -1;
+    if (t < used) {
+      // the last offset at most t belongs to a request that has tokens
+      req = in_sm ? last_at_most(cu_sm, p.n_req + 1, static_cast<int32_t>(t))
+                  : last_at_most(cu, p.n_req + 1, static_cast<int32_t>(t));
+      const int end = in_sm ? cu_sm[req + 1] : __ldcg(cu + req + 1);
+      pos = __ldcg(p.lens_out + req) - end + static_cast<int>(t);
+      const uint32_t pg = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page);
+      const int id = __ldcg(p.table + static_cast<int64_t>(req) * p.width + pg);
+      slot = id < 0 ? -1
+                    : static_cast<int>(id * p.page + (static_cast<uint32_t>(pos) - pg * p.page));
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+    p.requests[t] = req;
+  }
+}
+
+}  // namespace
+
+omq_status launch_plan(const PlanParams& p, cudaStream_t st) {
+  // one block while it can write the maps in a pass or two, then up to a portable cluster
+  const int cl = p.capacity <= 2 * kThreads ? 1 : p.capacity <= 8 * kThreads ? 4 : kMaxCluster;
+  launch_cl(kv_plan_kernel, cl, kThreads, 0, cl, st, p);
+  return launch_status();
+}
+
+}  // namespace kv
+}  // namespace omq

@@ -1,0 +1,553 @@
+// Attention of a few query rows over the 4-bit paged cache (decoding, drafted tokens), and, a
+// tile of rows at a time, of any number of rows.
+//
+// o = sum_j p_j v_j with p = softmax_j(scale q . k_j), k_j = (c - z) h and v_j alike. The codes
+// themselves are the matrix instructions' operands and the steps stay outside, in binary32:
+//   q . k_j       = h_j (sum_d q_d c_jd - z_j sum_d q_d)
+//   x_j           = scale log2(e) q . k_j + log2 hv_j,   w_j = 2^(x_j - max x)
+//   o             = (sum_j w_j cv_jd - sum_j w_j zv_j) / sum_j (w_j / hv_j)
+// so w_j = p_j hv_j up to the row's common factor lies in [0, 1] for any hv and its rounding to
+// float16 (the operand; the same rounded value weighs zv_j) is relative to the largest
+// contribution. A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
+// second nibble of a 16-bit lane: one AND makes two operands, exact, and the powers of two go
+// into q (the odd nibbles' q times 1/16; q itself scaled by a power of two per row, so every
+// input type is exact but for values 2^-28 below the row's largest) and into the result.
+//
+// Bound by the cache's bytes: D + 16 per token and kv head. One block per (request, kv head,
+// tile of 8 NB rows) and share of the tokens (a cluster splits them); each warp takes every
+// (blocks x warps)-th run of 64 tokens on its own: a ring of bulk copies (one per 16-token
+// cell, which holds codes and steps together), K as the 16 x 16 operand straight from 16-byte
+// shared loads, V transposed by ldmatrix, no barrier between warps until the end. Warps, then
+// blocks (through the cluster's shared memory) join their (max, sum, o) in a fixed order.
+#include "kv_internal.cuh"
+
+namespace omq {
+namespace kv {
+
+static __device__ unsigned g_rows_error = 0;
+static __device__ uint64_t g_rows_limit_ns = 2000000000ull;
+
+cudaError_t rows_take_error(unsigned* flag) {
+  unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(flag, g_rows_error, sizeof(unsigned));
+  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbol(g_rows_error, &zero, sizeof(unsigned));
+  return e;
+}
+cudaError_t rows_set_limit(uint64_t ns) {
+  return cudaMemcpyToSymbol(g_rows_limit_ns, &ns, sizeof(ns));
+}
+
+namespace {
+
+constexpr int W = 4;                  // warps of a block
+constexpr int STEP = 64;              // tokens of a run: four cells
+constexpr int NCELL = STEP / kCell;
+constexpr int STAGES = 3;
+
+template <int D, int NB>
+struct RowsCfg {
+  // cells 16 bytes further apart than they are long: the eight token rows of an ldmatrix come
+  // two from each of four cells and fall into eight different 16-byte bank groups (D = 128)
+  static constexpr int PITCH = CellT<D>::BYTES + 16;
+  static constexpr int STAGE = NCELL * PITCH;
+  static constexpr int RING = W * STAGES * STAGE;
+  static constexpr int R = 8 * NB;                      // query rows of a block
+  static constexpr int LDO = D + 4;                     // row stride of the partial outputs
+  static constexpr int PART = W * R * LDO * 4;          // the warps' partial outputs (ring reused)
+  static constexpr int BODY = RING > PART ? RING : PART;
+  static constexpr int STAT = BODY;                     // float [3][W][R]: max, sum, z sum
+  static constexpr int JOIN = STAT + 3 * W * R * 4;     // float [R][2] the block's (max, sum)
+  static constexpr int BARS = JOIN + R * 8;             // mbarriers [W][STAGES]
+  static constexpr int SMEM = BARS + W * STAGES * 8;
+};
+
+__device__ __forceinline__ float load_q(const void* q, int64_t i, omq_dtype dt) {
+  if (dt == OMQ_F16) return __half2float(static_cast<const __half*>(q)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+  const __half2 x = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles) {
+  using F = RowsCfg<D, NB>;
+  using C = CellT<D>;
+  constexpr int KM = D / 16;            // K-side matrix steps
+  constexpr int VM = D / 16;            // V-side row tiles
+  constexpr float kLog2e = 1.4426950408889634f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;
+  const int cl = static_cast<int>(cta_count()), rank = static_cast<int>(cta_rank());
+  const int item = blockIdx.x / cl;
+  const int tile = item % tiles;
+  const int kvh = (item / tiles) % p.pool.Hkv;
+  const int b = item / tiles / p.pool.Hkv;
+  const uint32_t bars = sb + F::BARS + warp * STAGES * 8;
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) bar_init(bars + 8 * s, 1);
+    bar_init_fence();
+  }
+  __syncwarp();
+  pdl_wait();
+  pdl_launch();
+
+  const int room = p.width * p.pool.page;
+  const int len = min(max(p.lens[b], 0), room);
+  const int first = p.cu[b];
+  const int n_new = min(max(p.cu[b + 1] - first, 0), p.max_q);
+  const int rows = n_new * p.G;
+  const int row0 = tile * F::R;
+  if (row0 >= rows || first < 0) return;               // the same for the whole cluster
+
+  // row r of the tile: new token (row0 + r) / G, query head kvh G + (row0 + r) mod G; it sees
+  // the first vis(r) tokens
+  auto row_ok = [&](int r) { return row0 + r < rows && first + (row0 + r) / p.G < p.T; };
+  auto row_at = [&](int r) {
+    const int i = (row0 + r) / p.G;
+    return static_cast<int64_t>(first + i) * p.q_ld +
+           static_cast<int64_t>(kvh * p.G + (row0 + r) - i * p.G) * D;
+  };
+  auto row_vis = [&](int r) {
+    if (!row_ok(r)) return 0;
+    return p.causal ? min(max(len - n_new + (row0 + r) / p.G + 1, 0), len) : len;
+  };
+  const int last_row = min(F::R, rows - row0) - 1;
+  const int vis_max = row_vis(last_row);
+  const int n_run = (vis_max + STEP - 1) / STEP;
+
+  // ---- q: this lane's operand values of query row 8 nb + g, its scale and its plain sum
+  uint32_t qf[NB][KM][2];
+  float cq[NB][2], sg[NB][2];           // of the lane's accumulator columns 2 tq, 2 tq + 1
+  int vis[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = 8 * nb + g;
+    const bool ok = row_ok(r);
+    const int64_t at = ok ? row_at(r) : 0;
+    // the row's largest magnitude: the lane's quarter of the row, then the four lanes
+    float am = 0.f;
+    for (int d = 0; d < D / 4; ++d) {
+      const float x = ok ? fabsf(load_q(p.q, at + tq * (D / 4) + d, p.dt)) : 0.f;
+      am = fmaxf(am, x);
+    }
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    int e = 0;
+    if (am > 0.f && am < INFINITY) e = 14 - ilogbf(am);
+    e = min(max(e, -100), 100);
+    const float up = ldexpf(1.f, e);
+    float sum = 0.f;
+#pragma unroll
+    for (int m = 0; m < KM; ++m) {
+      // matrix step m: word m / 2 of the lane's D / 4 values, nibble pairs (0, 4), (1, 5) or
+      // (2, 6), (3, 7)
+      const int d0 = tq * (D / 4) + 8 * (m >> 1) + 2 * (m & 1);
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = ok ? load_q(p.q, at + d0 + (j >> 1) + 4 * (j & 1), p.dt) * up : 0.f;
+      // the odd nibbles' codes stand 16 times too high
+      qf[nb][m][0] = h2(x[0], x[1]);
+      qf[nb][m][1] = h2(x[2] * 0.0625f, x[3] * 0.0625f);
+      const float2 u = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][0]));
+      const float2 v = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][1]));
+      sum += (u.x + u.y) + 16.f * (v.x + v.y);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    // x = h (acc cq - z sg): codes and q carry 2^-24 and 2^e
+    const float down = p.scale * kLog2e * ldexpf(1.f, -e);
+    const float my_cq = down * 16777216.f, my_sg = down * sum;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int src = 4 * (2 * tq + c);                  // a lane with g = 2 tq + c
+      cq[nb][c] = __shfl_sync(0xffffffffu, my_cq, src);
+      sg[nb][c] = __shfl_sync(0xffffffffu, my_sg, src);
+      vis[nb][c] = row_vis(8 * nb + 2 * tq + c);
+    }
+  }
+  const int vis_min = row_vis(0);       // the rows' least (those past the end are not stored)
+
+  float mx[NB][2], ls[NB][2], zs[NB][2];
+  float acc[NB][VM][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      mx[nb][c] = -INFINITY;
+      ls[nb][c] = 0.f;
+      zs[nb][c] = 0.f;
+    }
+#pragma unroll
+    for (int m = 0; m < VM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nb][m][i] = 0.f;
+  }
+
+  const uint32_t ring = sb + warp * STAGES * F::STAGE;
+  const int nw = cl * W, w0 = rank * W + warp;
+  const int32_t* row_table = p.table + static_cast<int64_t>(b) * p.width;
+  const int n_cell = (vis_max + kCell - 1) / kCell;
+  // Copies run `run` into stage s; returns which of its four cells exist (bit i: cell i).
+  auto fetch = [&](int run, int s) -> uint32_t {
+    const int ci = run * NCELL + lane;
+    int id = -1;
+    uint32_t pg = 0;
+    if (lane < NCELL && ci < n_cell) {
+      pg = static_cast<uint32_t>(ci) / static_cast<uint32_t>(p.pool.cells);
+      id = row_table[pg];
+    }
+    const bool have = id >= 0 && id < p.pool.n_pages;
+    const uint32_t mask = __ballot_sync(0xffffffffu, have);
+    if (lane == 0) bar_expect(bars + 8 * s, __popc(mask) * C::BYTES);
+    __syncwarp();
+    if (have) {
+      const uint8_t* src = p.pool.data + ((static_cast<int64_t>(id) * p.pool.Hkv + kvh) * p.pool.cells +
+                                          (ci - static_cast<int>(pg) * p.pool.cells)) *
+                                             static_cast<int64_t>(C::BYTES);
+      bulk_load(ring + s * F::STAGE + lane * F::PITCH, src, C::BYTES, bars + 8 * s);
+    }
+    return mask;
+  };
+
+  uint32_t have[STAGES];
+  int fetched = 0;
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) {
+    have[s] = 0;
+    if (s < STAGES - 1 && w0 + s * nw < n_run) {
+      have[s] = fetch(w0 + s * nw, s);
+      ++fetched;
+    }
+  }
+  bool ok = true;
+  int it = 0;
+  const int cell_i = g >> 1;                             // the lane's cell in K and P
+  for (int run = w0; run < n_run && ok; run += nw) {
+    // one stage per unrolled step, so that have[] stays in registers
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      if (run >= n_run) break;
+      if (s) {
+        run += nw;
+        if (run >= n_run) break;
+      }
+      const int ahead = run + (STAGES - 1) * nw;
+      if (ahead < n_run) {
+        have[(s + STAGES - 1) % STAGES] = fetch(ahead, (s + STAGES - 1) % STAGES);
+        ++fetched;
+      }
+      int got = 0;
+      if (lane == 0)
+        got = bar_wait(bars + 8 * s, (it / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
+                       DEV_ERR_TMA_WAIT);
+      got = __shfl_sync(0xffffffffu, got, 0);
+      // every lane observes the completed phase itself before it reads what the copies wrote
+      if (!got || !bar_try(bars + 8 * s, (it / STAGES) & 1)) got = 0;
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      ++it;
+      const uint32_t st = ring + s * F::STAGE;
+      const uint32_t cell = st + cell_i * F::PITCH;
+      const int t0 = run * STEP + kCell * cell_i + (g & 1);    // + 4 s' + 2 a: the lane's tokens
+      const bool cell_ok = (have[s] >> cell_i) & 1u;
+      const bool edge = run * STEP + STEP > vis_min;
+
+      // ---- scores of the lane's 8 tokens x 2 NB queries
+      float x[NB][8][2];
+#pragma unroll
+      for (int ms = 0; ms < 4; ++ms) {
+        float sacc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sacc[nb][i] = 0.f;
+        const int tok = 4 * ms + (g & 1);                 // and tok + 2
+        const uint32_t ka = cell + C::K + tok * C::ROW + tq * (C::ROW / 4);
+        uint32_t wa[D / 32], wb[D / 32];
+        if constexpr (D == 128) {
+          const uint4 u = lds128(ka), v = lds128(ka + 2 * C::ROW);
+          wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
+          wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
+        } else {
+          const uint2 u = lds64(ka), v = lds64(ka + 2 * C::ROW);
+          wa[0] = u.x; wa[1] = u.y;
+          wb[0] = v.x; wb[1] = v.y;
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816(sacc[nb], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u,
+                     wb[w] & 0x00F000F0u, qf[nb][2 * w][0], qf[nb][2 * w][1]);
+            mma16816(sacc[nb], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                     b8 & 0x00F000F0u, qf[nb][2 * w + 1][0], qf[nb][2 * w + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          x[nb][2 * ms][0] = sacc[nb][0];
+          x[nb][2 * ms][1] = sacc[nb][1];
+          x[nb][2 * ms + 1][0] = sacc[nb][2];
+          x[nb][2 * ms + 1][1] = sacc[nb][3];
+        }
+      }
+      // steps of the lane's tokens; a token that is not there has no weight and a finite step
+      float rh[8], vz[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int tok = 2 * j + (g & 1);
+        float kh = lds_f(cell + C::KH + 4 * tok), kz = static_cast<float>(lds_i(cell + C::KZ + 4 * tok));
+        float vh = lds_f(cell + C::VH + 4 * tok);
+        vz[j] = static_cast<float>(lds_i(cell + C::VZ + 4 * tok));
+        const bool there = cell_ok && t0 + 2 * j < vis_max;
+        if (!there) {
+          kh = 0.f;
+          kz = 0.f;
+          vh = 1.f;
+          vz[j] = 0.f;
+        }
+        const float lh = __log2f(vh);
+        // a NaN step reaches the rows that see the token through lh, and only those
+        rh[j] = vh == vh ? __frcp_rn(vh) : 1.f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float t = __fmaf_rn(x[nb][j][c], cq[nb][c], -kz * sg[nb][c]);
+            float v = __fmaf_rn(t, kh, lh);
+            if (edge || !cell_ok) v = (there && t0 + 2 * j < vis[nb][c]) ? v : -INFINITY;
+            x[nb][j][c] = v;
+          }
+      }
+      // ---- running maximum, weights, sums
+      uint32_t pw[NB][4][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float al[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = x[nb][0][c];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) m = fmaxf(m, x[nb][j][c]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          m = fmaxf(m, mx[nb][c]);
+          const float ref = m == -INFINITY ? 0.f : m;
+          al[c] = ex2(mx[nb][c] - ref);
+          mx[nb][c] = m;
+          float l = 0.f, zz = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float w = ex2(x[nb][j][c] - ref);
+            l = __fmaf_rn(w, rh[j], l);
+            x[nb][j][c] = w;
+          }
+          ls[nb][c] = __fmaf_rn(ls[nb][c], al[c], l);
+          // the weights as the matrix instruction takes them
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            zz = __fmaf_rn(__half2float(__float2half_rn(x[nb][j][c])), vz[j], zz);
+          zs[nb][c] = __fmaf_rn(zs[nb][c], al[c], zz);
+        }
+#pragma unroll
+        for (int ms = 0; ms < 4; ++ms)
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+            pw[nb][ms][a] = movm_t(h2(x[nb][2 * ms + a][0], x[nb][2 * ms + a][1]));
+        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+          for (int m = 0; m < VM; ++m) {
+            acc[nb][m][0] *= al[0];
+            acc[nb][m][1] *= al[1];
+            acc[nb][m][2] *= al[0];
+            acc[nb][m][3] *= al[1];
+          }
+        }
+      }
+      // ---- o^T += V^T w: V's 8 x 8 blocks transposed on their way to registers
+#pragma unroll
+      for (int ms = 0; ms < 4; ++ms) {
+#pragma unroll
+        for (int jj = 0; jj < D / 64; ++jj) {
+          // matrices: (tokens a = 0, columns 2 jj), (a = 1, 2 jj), (0, 2 jj + 1), (1, 2 jj + 1)
+          const int mi = lane >> 3, r = lane & 7;
+          const uint32_t va = st + (r >> 1) * F::PITCH + C::V +
+                              (4 * ms + 2 * (mi & 1) + (r & 1)) * C::ROW + 16 * (2 * jj + (mi >> 1));
+          uint32_t v[4];
+          ldsm4_t(va, v);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t lo = v[2 * q], hi = v[2 * q + 1];
+            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+            const int m = 2 * (2 * jj + q);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(acc[nb][m], lo & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x000F000Fu,
+                       hi & 0x00F000F0u, pw[nb][ms][0], pw[nb][ms][1]);
+              mma16816(acc[nb][m + 1], lo8 & 0x000F000Fu, lo8 & 0x00F000F0u, hi8 & 0x000F000Fu,
+                       hi8 & 0x00F000F0u, pw[nb][ms][0], pw[nb][ms][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();                                      // the stage may be written again
+    }
+  }
+  if (!ok) {                                             // copies in flight land before the end
+    if (lane == 0)
+      for (int j = it; j < fetched; ++j)
+        bar_wait(bars + 8 * (j % STAGES), (j / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
+                 DEV_ERR_TMA_WAIT);
+    __syncwarp();
+  }
+
+  // ---- join the warps
+  float* stat = reinterpret_cast<float*>(smem + F::STAT);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        ls[nb][c] += __shfl_xor_sync(0xffffffffu, ls[nb][c], o);
+        zs[nb][c] += __shfl_xor_sync(0xffffffffu, zs[nb][c], o);
+      }
+      if (g == 0) {
+        const int r = 8 * nb + 2 * tq + c;
+        stat[(0 * W + warp) * F::R + r] = mx[nb][c];
+        stat[(1 * W + warp) * F::R + r] = ls[nb][c];
+      }
+    }
+  __syncthreads();                                       // the ring's last readers are done, too
+  float* part = reinterpret_cast<float*>(smem);          // [W][R][LDO]
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * nb + 2 * tq + c;
+      float m = stat[r];
+#pragma unroll
+      for (int w = 1; w < W; ++w) m = fmaxf(m, stat[w * F::R + r]);
+      const float f = mx[nb][c] == -INFINITY ? 0.f : ex2(mx[nb][c] - m);
+#pragma unroll
+      for (int q = 0; q < VM; ++q) {
+        // row tile q: columns 32 (q / 2) + 4 g + e, e = 2 (q & 1) and the next (16 times high)
+        const int d = 32 * (q >> 1) + 4 * g + 2 * (q & 1);
+        float2 o;
+        o.x = (acc[nb][q][c] * 16777216.f - zs[nb][c]) * f;
+        o.y = (acc[nb][q][2 + c] * 1048576.f - zs[nb][c]) * f;
+        *reinterpret_cast<float2*>(part + (warp * F::R + r) * F::LDO + d) = o;
+      }
+    }
+  __syncthreads();
+  float* join = reinterpret_cast<float*>(smem + F::JOIN);
+  if (threadIdx.x < F::R) {
+    const int r = threadIdx.x;
+    float m = stat[r];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = fmaxf(m, stat[w * F::R + r]);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float mw = stat[w * F::R + r];
+      // without a key the sum is 0, or NaN where a key was NaN: both survive the product
+      l += stat[(W + w) * F::R + r] * (mw == -INFINITY ? 0.f : ex2(mw - m));
+    }
+    join[2 * r] = m;
+    join[2 * r + 1] = l;
+  }
+  for (int i = threadIdx.x; i < F::R * (D / 2); i += 32 * W) {
+    const int r = i / (D / 2), d = 2 * (i % (D / 2));
+    float2 s = *reinterpret_cast<float2*>(part + r * F::LDO + d);
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float2 u = *reinterpret_cast<float2*>(part + (w * F::R + r) * F::LDO + d);
+      s.x += u.x;
+      s.y += u.y;
+    }
+    *reinterpret_cast<float2*>(part + r * F::LDO + d) = s;
+  }
+  // ---- join the cluster's blocks: each finishes its share of the tile's values
+  if (cl > 1) cluster_sync_all();
+  else __syncthreads();
+  const int n_val = F::R * (D / 2), share = (n_val + cl - 1) / cl;
+  const int hi = min(n_val, (rank + 1) * share);
+  for (int i = rank * share + static_cast<int>(threadIdx.x); i < hi; i += 32 * W) {
+    const int r = i / (D / 2), d = 2 * (i % (D / 2));
+    if (!row_ok(r)) continue;
+    const uint32_t ja = sb + F::JOIN + 8 * r, pa = sb + (r * F::LDO + d) * 4;
+    float m = -INFINITY;
+    for (int k = 0; k < cl; ++k) m = fmaxf(m, ld_cluster(map_rank(ja, k)));
+    float l = 0.f, ox = 0.f, oy = 0.f;
+    for (int k = 0; k < cl; ++k) {
+      const float2 ml = ld_cluster2(map_rank(ja, k));
+      const float2 o = ld_cluster2(map_rank(pa, k));
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+      l = __fmaf_rn(ml.y, f, l);
+      ox = __fmaf_rn(o.x, f, ox);
+      oy = __fmaf_rn(o.y, f, oy);
+    }
+    const bool none = l == 0.f;                          // a visible key adds 1 / hv or NaN
+    const float inv = none ? 0.f : 1.f / l;
+    const float yx = none ? 0.f : ox * inv, yy = none ? 0.f : oy * inv;
+    const int tok = (row0 + r) / p.G;
+    const int64_t orow = static_cast<int64_t>(first + tok) * p.Hq + kvh * p.G + (row0 + r) - tok * p.G;
+    uint32_t packed;
+    if (p.out_dt == OMQ_F16) packed = h2(yx, yy);
+    else {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(yx, yy);
+      packed = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = packed;
+    if (p.lse && d == 0)
+      p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
+  }
+  if (cl > 1) cluster_sync_all();                        // no block leaves while it is read
+}
+
+template <int D, int NB>
+omq_status launch_rows(const AttnParams& p, cudaStream_t st) {
+  using F = RowsCfg<D, NB>;
+  static thread_local int ready = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (ready != dev) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_rows_kernel<D, NB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+    if (e != cudaSuccess) {
+      set_cuda_error(e);
+      return OMQ_ERR_CUDA;
+    }
+    ready = dev;
+  }
+  const int64_t max_rows = static_cast<int64_t>(p.max_q) * p.G;
+  const int64_t tiles = ceil_div(max_rows, F::R);
+  const int64_t items = tiles * p.pool.Hkv * p.n_req;
+  const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
+  // split the tokens while there are fewer blocks than the SMs hold and a warp keeps a run
+  int cl = 1;
+  while (cl < kMaxCluster && items * cl < 2 * num_sms() && 2 * cl * W <= runs) cl *= 2;
+  launch_cl(kv_rows_kernel<D, NB>, dim3(static_cast<unsigned>(items * cl)), 32 * W, F::SMEM, cl, st,
+            p, static_cast<int>(tiles));
+  return launch_status();
+}
+
+}  // namespace
+
+omq_status launch_attn_rows(const AttnParams& p, int64_t D, cudaStream_t st) {
+  const bool one = static_cast<int64_t>(p.max_q) * p.G <= 8;
+  if (D == 128) return one ? launch_rows<128, 1>(p, st) : launch_rows<128, 2>(p, st);
+  return one ? launch_rows<64, 1>(p, st) : launch_rows<64, 2>(p, st);
+}
+
+}  // namespace kv
+}  // namespace omq

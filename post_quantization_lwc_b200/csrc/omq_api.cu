@@ -5,6 +5,7 @@
 #include <mutex>
 #include <vector>
 
+#include "kv_internal.cuh"
 #include "omq_internal.cuh"
 
 namespace omq {
@@ -231,7 +232,8 @@ int omq_version(void) { return 10000; }
 
 omq_status omq_set_wait_limit_ns(uint64_t ns) {
   if (ns < 1000000ull || ns > 60000000000ull) return OMQ_ERR_SHAPE;
-  const cudaError_t e = set_wait_limit(ns);
+  cudaError_t e = set_wait_limit(ns);
+  if (e == cudaSuccess) e = kv::rows_set_limit(ns);
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;
@@ -254,8 +256,10 @@ omq_status omq_sync_check(omq_stream_t stream) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;
   }
-  unsigned flag = 0;
+  unsigned flag = 0, kv_flag = 0;
   e = take_device_error(&flag);
+  if (e == cudaSuccess) e = kv::rows_take_error(&kv_flag);
+  flag |= kv_flag;
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;

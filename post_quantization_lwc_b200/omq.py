@@ -33,7 +33,9 @@ EXPORTS = ("omq_status_str", "omq_last_cuda_error", "omq_version", "omq_sync_che
            "omq_fq_linear_fwd_noalloc", "omq_block_theta_range", "omq_block_buffer",
            "omq_block_workspace_bytes", "omq_block_step", "omq_block_reference",
            "omq_block_quant_forward", "omq_block_calibrate", "omq_qgemv",
-           "omq_set_wait_limit_ns", "omq_wait_limit_ns", "omq_wait_probe", "omq_qgemm")
+           "omq_set_wait_limit_ns", "omq_wait_limit_ns", "omq_wait_probe", "omq_qgemm",
+           "omq_kv_cell_bytes", "omq_rope_table", "omq_kv_plan", "omq_kv_append", "omq_kv_read",
+           "omq_kv_attn", "omq_kv_attn_workspace_bytes")
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -95,6 +97,31 @@ class BlockCalibArgs(ctypes.Structure):
                 ("first_step", _i64), ("lr_lwc", _f32), ("lr_let", _f32), ("losses", _p)]
 
 
+class KvPool(ctypes.Structure):
+    _fields_ = [("data", _p), ("n_pages", _i64), ("page", _i64), ("Hkv", _i64), ("D", _i64)]
+
+
+class KvPlanArgs(ctypes.Structure):
+    _fields_ = [("lens", _p), ("new_tokens", _p), ("n_req", _i64), ("table", _p), ("width", _i64),
+                ("page", _i64), ("free_pages", _p), ("n_pages", _i64), ("n_free", _p),
+                ("lens_out", _p), ("n_free_out", _p), ("cu", _p), ("slots", _p),
+                ("positions", _p), ("requests", _p), ("capacity", _i64)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("pool", KvPool), ("T", _i64), ("Hq", _i64), ("dt", _i32), ("q", _p), ("k", _p),
+                ("v", _p), ("q_ld", _i64), ("k_ld", _i64), ("v_ld", _i64), ("slots", _p),
+                ("positions", _p), ("rope", _p), ("n_pos", _i64), ("s_a", _p), ("s_o", _p),
+                ("delta_o", _p), ("abits", _i32), ("q_out", _p), ("q_dt", _i32)]
+
+
+class KvAttnArgs(ctypes.Structure):
+    _fields_ = [("pool", KvPool), ("n_req", _i64), ("T", _i64), ("Hq", _i64), ("q", _p),
+                ("q_ld", _i64), ("dt", _i32), ("table", _p), ("width", _i64), ("lens", _p),
+                ("cu", _p), ("max_q", _i64), ("scale", _f32), ("causal", _i32), ("out", _p),
+                ("out_dt", _i32), ("lse", _p)]
+
+
 # phases of omq_calib_step (OMQ_PH_* in include/omq.h), in order
 PHASES = ("let", "lwc", "fwd_gemm", "loss", "dbias", "dw_gemm", "ste_w", "dx_gemm", "ste_x",
           "let_reduce", "adamw")
@@ -140,6 +167,13 @@ _sig("omq_set_wait_limit_ns", _i32, [ctypes.c_uint64])
 _sig("omq_wait_limit_ns", ctypes.c_uint64, [])
 _sig("omq_wait_probe", _i32, [_i32, _p])
 _sig("omq_qgemm", _i32, [_p, _i32, _i64, _i64, _p, _p, _p, _i64, _i64, _i32, _p, _p, _p])
+_sig("omq_kv_cell_bytes", _sz, [_i64])
+_sig("omq_rope_table", _i32, [_i64, _i64, ctypes.c_double, _p, _p])
+_sig("omq_kv_plan", _i32, [ctypes.POINTER(KvPlanArgs), _p])
+_sig("omq_kv_append", _i32, [ctypes.POINTER(KvAppendArgs), _p])
+_sig("omq_kv_read", _i32, [ctypes.POINTER(KvPool), _i64, _p, _p, _p, _i32, _p])
+_sig("omq_kv_attn", _i32, [ctypes.POINTER(KvAttnArgs), _p, _sz, _p])
+_sig("omq_kv_attn_workspace_bytes", _sz, [ctypes.POINTER(KvAttnArgs)])
 
 
 def _check(status: int, where: str):
@@ -372,6 +406,194 @@ def qgemm(x, packed, h, z, group, bits, bias=None, stream=None):
     _check(_lib.omq_qgemm(_ptr(x), _dt(x), M, K, _ptr(packed), _ptr(h), _ptr(z), N, group, bits,
                           _ptr(bias), _ptr(y), _stream(stream)), "omq_qgemm")
     return y
+
+
+# ---------------------------------------------------------------------------- 4-bit KV cache
+
+def kv_cell_bytes(D) -> int:
+    """Bytes of a 16-token cell of one kv head (0: head size not supported)."""
+    return int(_lib.omq_kv_cell_bytes(D))
+
+
+def kv_pool(n_pages, Hkv, D, page, device="cuda") -> torch.Tensor:
+    """Storage of a 4-bit paged key/value cache: uint8 [n_pages, Hkv, page / 16, cell]."""
+    if kv_cell_bytes(D) == 0 or page < 16 or page % 16:
+        raise ValueError("D is 64 or 128, page a multiple of 16")
+    return torch.empty(n_pages, Hkv, page // 16, kv_cell_bytes(D), dtype=torch.uint8,
+                       device=device)
+
+
+def _pool(pool) -> KvPool:
+    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_cuda or not pool.is_contiguous():
+        raise ValueError("the pool is a contiguous CUDA uint8 [n_pages, Hkv, page / 16, cell] tensor")
+    n, hkv, cells, cell = pool.shape
+    return KvPool(pool.data_ptr(), n, 16 * cells, hkv, (cell - 256) // 16)
+
+
+def _ints(device, *ts):
+    for t in ts:
+        if t is not None and (t.dtype != torch.int32 or t.device != device or
+                              not t.is_contiguous()):
+            raise ValueError("lengths, tables, slots and positions are contiguous int32 tensors "
+                             "on the pool's device")
+
+
+def _rows(device, t, D):
+    """Token stride of a [T, heads, D] tensor whose heads lie back to back."""
+    if t.device != device or t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or \
+            (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError("q, k and v are [T, heads, D] CUDA tensors, a token's heads back to back")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def rope_table(n_pos, D, base=10000.0, device="cuda", stream=None) -> torch.Tensor:
+    """omq_rope_table: float32 [2, n_pos, D/2], cos and sin of position * base^(-2i/D)."""
+    t = torch.empty(2, n_pos, D // 2, dtype=torch.float32, device=device)
+    with torch.cuda.device(t.device):
+        _check(_lib.omq_rope_table(n_pos, D, float(base), _ptr(t), _stream(stream)),
+               "omq_rope_table")
+    return t
+
+
+def kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_place=False,
+            stream=None):
+    """omq_kv_plan: one step's pages, slots and positions from the requests' lengths. table and
+    free_pages are updated in place, lens and n_free with ``in_place`` (else new tensors).
+    Returns dict(lens, n_free, cu, slots, positions, requests)."""
+    dev = lens.device
+    if not lens.is_cuda:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    _ints(dev, lens, new_tokens, table, free_pages, n_free)
+    B = lens.numel()
+    if table.dim() != 2 or table.shape[0] != B or new_tokens.numel() != B or n_free.numel() != 1:
+        raise ValueError("lens and new_tokens are [n_req], table [n_req, width], n_free [1]")
+    own = 0 if in_place else B + 1
+    # one allocation: cu, the token maps, and the new lengths
+    buf = torch.empty(B + 1 + 3 * max(capacity, 0) + own, dtype=torch.int32, device=dev)
+    cu, slots, positions, requests, rest = buf.split_with_sizes(
+        [B + 1, capacity, capacity, capacity, own])
+    lens_out, n_free_out = (lens, n_free) if in_place else rest.split_with_sizes([B, 1])
+    a = KvPlanArgs(lens.data_ptr(), new_tokens.data_ptr(), B, table.data_ptr(), table.shape[1],
+                   page, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                   lens_out.data_ptr(), n_free_out.data_ptr(), cu.data_ptr(), slots.data_ptr(),
+                   positions.data_ptr(), requests.data_ptr(), capacity)
+    with torch.cuda.device(dev):
+        _check(_lib.omq_kv_plan(ctypes.byref(a), _stream(stream)), "omq_kv_plan")
+    return dict(lens=lens_out, n_free=n_free_out, cu=cu, slots=slots, positions=positions,
+                requests=requests)
+
+
+def kv_append(pool, slots, k, v, q=None, positions=None, rope=None, s_a=None, s_o=None,
+              delta_o=None, abits=16, q_dtype=torch.float16, q_out=None, stream=None):
+    """omq_kv_append: k, v [T, Hkv, D] (token stride free) rotated, scaled, quantized to 4 bits
+    and stored at slots [T]. With q [T, Hq, D]: returns q~ [T, Hq, D] (into q_out if given)."""
+    P = _pool(pool)
+    dev = pool.device
+    _ints(dev, slots, positions)
+    T = slots.numel()
+    ld = [0 if t is None else _rows(dev, t, P.D) for t in (q, k, v)]
+    if k.shape[0] != T or v.shape != k.shape or k.shape[1] != P.Hkv or k.dtype != v.dtype or \
+            (q is not None and (q.shape[0] != T or q.dtype != k.dtype)) or \
+            (positions is not None and positions.numel() != T):
+        raise ValueError("q, k, v, slots and positions disagree in tokens, heads or type")
+    for t in (s_a, s_o, delta_o):
+        if t is not None and (t.dtype != torch.float32 or t.device != dev or
+                              not t.is_contiguous() or t.numel() != P.Hkv * P.D):
+            raise ValueError("s_a, s_o and delta_o are contiguous float32 [Hkv, D]")
+    if rope is not None and (rope.dtype != torch.float32 or rope.device != dev or rope.dim() != 3 or
+                             not rope.is_contiguous() or rope.shape[0] != 2 or
+                             rope.shape[2] != P.D // 2):
+        raise ValueError("rope is a contiguous float32 [2, n_pos, D / 2]")
+    if rope is not None and positions is None:
+        raise ValueError("a rotary table needs positions")
+    Hq = 0 if q is None else q.shape[1]
+    if q is not None and q_out is None:
+        q_out = torch.empty(T, Hq, P.D, dtype=q_dtype, device=dev)
+    elif q_out is not None and (q is None or q_out.shape != q.shape or q_out.device != dev or
+                                not q_out.is_contiguous()):
+        raise ValueError("q_out is contiguous, of q's shape")
+    pt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    a = KvAppendArgs(P, T, Hq, _dt(k), pt(q), k.data_ptr(), v.data_ptr(), ld[0], ld[1], ld[2],
+                     slots.data_ptr(), pt(positions), pt(rope), 0 if rope is None else rope.shape[1],
+                     pt(s_a), pt(s_o), pt(delta_o), abits, pt(q_out),
+                     0 if q is None else _dt(q_out))
+    with torch.cuda.device(dev):
+        _check(_lib.omq_kv_append(ctypes.byref(a), _stream(stream)), "omq_kv_append")
+    return q_out
+
+
+def kv_read(pool, slots, dtype=torch.float32, stream=None):
+    """omq_kv_read: the stored (k, v), each [T, Hkv, D], of the slots."""
+    P = _pool(pool)
+    _ints(pool.device, slots)
+    T = slots.numel()
+    k, v = (torch.empty(T, P.Hkv, P.D, dtype=dtype, device=pool.device) for _ in range(2))
+    with torch.cuda.device(pool.device):
+        _check(_lib.omq_kv_read(ctypes.byref(P), T, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                _dt(k), _stream(stream)), "omq_kv_read")
+    return k, v
+
+
+def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, out_dtype=None,
+            lse=False, stream=None):
+    """omq_kv_attn: attention of q [T, Hq, D] (the requests' rows per cu) over the cache; rows
+    of a new `out` behind the last request are not written. Returns out [T, Hq, D], or
+    (out, lse [T, Hq]) with ``lse``."""
+    P = _pool(pool)
+    dev = pool.device
+    _ints(dev, table, lens, cu)
+    ld = _rows(dev, q, P.D)
+    B = lens.numel()
+    if table.dim() != 2 or table.shape[0] != B or cu.numel() != B + 1:
+        raise ValueError("lens is [n_req], table [n_req, width], cu [n_req + 1]")
+    T, Hq = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(T, Hq, P.D, dtype=out_dtype or q.dtype, device=dev)
+    elif out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise ValueError("out is contiguous, of q's shape")
+    ls = torch.empty(T, Hq, dtype=torch.float32, device=dev) if lse else None
+    a = KvAttnArgs(P, B, T, Hq, q.data_ptr(), ld, _dt(q), table.data_ptr(), table.shape[1],
+                   lens.data_ptr(), cu.data_ptr(), max_q,
+                   P.D ** -0.5 if scale is None else scale, 1 if causal else 0, out.data_ptr(),
+                   _dt(out), None if ls is None else ls.data_ptr())
+    with torch.cuda.device(dev):
+        n = _lib.omq_kv_attn_workspace_bytes(ctypes.byref(a))
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        _check(_lib.omq_kv_attn(ctypes.byref(a), _ptr(ws), n, _stream(stream)), "omq_kv_attn")
+    return (out, ls) if lse else out
+
+
+class KVCache:
+    """A 4-bit paged key/value cache and its requests' state on the device: the pool, the block
+    table, the lengths and the stack of free pages. One serving step is ``plan`` (pages, slots
+    and positions of the step's new tokens), ``append`` (their k and v, and q made ready) and
+    ``attend``; all of it may be captured in a CUDA graph, with ``new_tokens`` and the
+    activations in fixed buffers."""
+
+    def __init__(self, n_req, n_pages, Hkv, D, page=64, max_len=4096, n_pos=None, base=10000.0,
+                 device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.pool = kv_pool(n_pages, Hkv, D, page, device)
+        self.page = page
+        self.table = torch.full((n_req, -(-max_len // page)), -1, **i32)
+        self.lens = torch.zeros(n_req, **i32)
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, **i32)     # page 0 on top
+        self.n_free = torch.full((1,), n_pages, **i32)
+        self.rope = rope_table(n_pos or max_len, D, base, device)
+
+    def plan(self, new_tokens, capacity, stream=None):
+        """omq_kv_plan in place: dict(lens, n_free, cu, slots, positions, requests)."""
+        return kv_plan(self.lens, new_tokens, self.table, self.free_pages, self.n_free, self.page,
+                       capacity, in_place=True, stream=stream)
+
+    def append(self, step, k, v, q=None, **kw):
+        """omq_kv_append of the step's rows, rotated to their positions; q~ when q is given."""
+        return kv_append(self.pool, step["slots"], k, v, q=q, positions=step["positions"],
+                         rope=self.rope, **kw)
+
+    def attend(self, step, q, max_q, **kw):
+        """omq_kv_attn of the step's queries."""
+        return kv_attn(q, self.pool, self.table, self.lens, step["cu"], max_q, **kw)
 
 
 def step_workspace_bytes(M, N, K, group) -> int:

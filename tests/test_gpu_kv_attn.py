@@ -1,0 +1,237 @@
+"""omq_kv_attn against the binary64 attention over the stored values, element by element within
+the error bound of tests/kv_common.py:attend (derived there, before any run): every shape class
+the entry point takes (single rows, drafted tokens, chunks, whole prompts; ragged lengths from
+0 on; pages that end inside a tile; rows without a key), with the pool's unused slots full of
+NaN steps."""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv_common as kc
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def omq(cuda_device):
+    from post_quantization_lwc_b200 import build
+    build.build()
+    from post_quantization_lwc_b200 import omq as m
+    return m
+
+
+class Setup:
+    """Requests with lens keys and new queries each over a shuffled table; slots no request owns
+    (and those behind a request's last token) hold 0xFF bytes: codes 15, steps NaN."""
+
+    def __init__(self, dev, lens, new, Hkv, G, D, page, dt, seed=0, far=None, spread=1.0, extra_rows=0,
+                 shift=0.0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.new = np.asarray(lens), np.asarray(new)
+        self.Hkv, self.G, self.D, self.page = Hkv, G, D, page
+        need = -(-np.maximum(self.lens, 0) // page)
+        width = max(1, int(need.max()) + 1)
+        n_pages = int(need.sum()) + 2
+        ids = rng.permutation(n_pages)
+        self.table = np.full((len(lens), width), -1, np.int32)
+        self.kv = []
+        pool = np.full((n_pages, Hkv, page // 16, kc.cell_bytes(D)), 255, np.uint8)
+        at = 0
+        for b, n in enumerate(self.lens):
+            self.table[b, :need[b]] = ids[at:at + need[b]]
+            at += need[b]
+            k = rng.standard_normal((n, Hkv, D)) * np.exp(0.5 * rng.standard_normal((Hkv, D))) * spread
+            v = rng.standard_normal((n, Hkv, D)) * np.exp(rng.standard_normal((n, 1, 1))) + shift
+            rows = [kc.encode(x.astype(np.float32)) for x in (k, v)]
+            pos = np.arange(n)
+            slots = self.table[b, pos // page] * page + pos % page
+            for w in range(2):
+                self.put(pool, slots, w, *rows[w])
+            self.kv.append(rows)
+        self.cu = np.concatenate(([0], np.cumsum(self.new))).astype(np.int32)
+        self.T = int(self.cu[-1]) + extra_rows
+        gen = torch.Generator().manual_seed(seed)
+        self.q = torch.randn(max(self.T, 1), Hkv * G, D, generator=gen).to(DT[dt])
+        if far is not None:                       # rows of very different size
+            self.q *= torch.exp2(torch.randint(-far, far, (max(self.T, 1), Hkv * G, 1), generator=gen)).to(self.q.dtype)
+        self.dev, self.pool_np = dev, pool
+        self.pool = torch.from_numpy(pool).to(dev)
+        i = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(dev)  # noqa: E731
+        self.args = [self.q.to(dev), self.pool, i(self.table), i(self.lens), i(self.cu)]
+        self.max_q = max(1, int(self.new.max()))
+
+    def put(self, pool, slots, w, c, h, z):
+        """kc.put, vectorised."""
+        D, half = self.D, kc.CELL * self.D // 2
+        p, off = np.divmod(slots, self.page)
+        cell, r = np.divmod(off, kc.CELL)
+        code = c.astype(np.uint8)
+        by = code[..., 0::2] | (code[..., 1::2] << 4)
+        codes = pool[..., w * half:(w + 1) * half].reshape(*pool.shape[:3], kc.CELL, D // 2)
+        codes[p, :, cell, r] = by
+        pool[..., w * half:(w + 1) * half] = codes.reshape(*pool.shape[:3], half)
+        for off_, x, t in ((0, h, np.float32), (64, z, np.int32)):
+            a = 2 * half + 128 * w + off_
+            m = np.ascontiguousarray(pool[..., a:a + 64]).view(t)
+            m[p, :, cell, r] = x[..., 0].astype(t)
+            pool[..., a:a + 64] = m.view(np.uint8).reshape(*pool.shape[:3], 64)
+
+    def check(self, out, lse=None, causal=True, scale=None, rows=None, hidden=()):
+        """Every row (or every `rows`-th of a request) of every head against the statement.
+        hidden: (request, page index) pairs whose table entries are not pages."""
+        scale = self.D ** -0.5 if scale is None else scale
+        eps = torch.finfo(out.dtype).eps / 2
+        got = out.double().cpu().numpy()
+        got_l = None if lse is None else lse.double().cpu().numpy()
+        worst = 0.0
+        for b in range(len(self.lens)):
+            n, m = int(self.lens[b]), int(self.new[b])
+            there = np.ones(n, bool)
+            for rb, pg in hidden:
+                if rb == b:
+                    there[pg * self.page:(pg + 1) * self.page] = False
+            pick = range(m) if rows is None else sorted({0, m - 1, *range(0, m, rows)} if m else ())
+            for i in pick:
+                seen = there & (np.arange(n) <= n - m + i) if causal else there
+                t = int(self.cu[b]) + i
+                for h in range(self.Hkv * self.G):
+                    kh = h // self.G
+                    (a, ah, az), (c, ch, cz) = self.kv[b]
+                    o, l, tol, ltol = kc.attend(self.q[t, h].double().numpy(), a[:, kh], ah[:, kh], az[:, kh],
+                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps)
+                    err = np.abs(got[t, h] - o)
+                    assert np.all(err <= tol), (b, i, h, float((err - tol).max()), float(err.max()))
+                    worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()))
+                    if got_l is not None:
+                        assert (got_l[t, h] == l) if np.isinf(l) else abs(got_l[t, h] - l) <= ltol, (b, i, h)
+        return worst
+
+
+SMALL = [  # lens, new, Hkv, G, D, page, dtype
+    ([1], [1], 1, 1, 128, 16, "f16"),
+    ([0, 1, 2], [0, 1, 1], 2, 1, 64, 16, "bf16"),
+    ([15, 16, 17, 63, 64, 65], [1] * 6, 2, 4, 128, 16, "bf16"),
+    ([47, 48, 49, 96, 200, 1], [1] * 6, 1, 8, 128, 48, "f16"),
+    ([130, 7, 300, 257], [1] * 4, 3, 7, 64, 64, "f16"),
+    ([1023, 31], [1, 1], 1, 3, 128, 128, "bf16"),
+    ([5, 64, 130], [5, 5, 5], 2, 2, 64, 32, "f16"),
+    ([5, 64, 130, 9], [3, 1, 8, 0], 2, 4, 128, 16, "bf16"),
+    ([20, 33, 150], [20, 17, 40], 1, 1, 128, 16, "f16"),
+    ([129, 300], [129, 130], 2, 4, 128, 64, "bf16"),
+    ([260, 140, 3], [259, 33, 3], 1, 7, 64, 48, "f16"),
+    ([600], [1], 2, 16, 128, 64, "bf16"),
+    ([400, 128], [70, 128], 1, 16, 64, 16, "bf16"),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,new,Hkv,G,D,page,dt", SMALL)
+def test_attention(omq, cuda_device, lens, new, Hkv, G, D, page, dt, causal):
+    s = Setup(cuda_device, lens, new, Hkv, G, D, page, dt, seed=len(lens) + D)
+    out, lse = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
+    omq.sync_check()
+    s.check(out, lse, causal, rows=None if sum(new) * Hkv * G < 400 else 13)
+
+
+@pytest.mark.parametrize("lens,new,Hkv,G,D,page,dt", [
+    ([4099, 2000], [1, 1], 2, 4, 128, 64, "bf16"),
+    ([20011], [1], 1, 8, 128, 16, "f16"),
+    ([9000], [4], 1, 2, 64, 128, "f16"),
+    ([3000, 5], [700, 5], 1, 4, 128, 64, "bf16"),
+    ([2048], [2048], 2, 1, 128, 16, "bf16"),
+    ([1500, 1411, 2047], [500, 1, 257], 1, 2, 64, 32, "f16")])
+def test_long_contexts(omq, cuda_device, lens, new, Hkv, G, D, page, dt):
+    s = Setup(cuda_device, lens, new, Hkv, G, D, page, dt, seed=7)
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse, rows=97)
+
+
+@pytest.mark.parametrize("new", [1, 6, 150])
+def test_other_types_scales_and_sizes(omq, cuda_device, new):
+    """Output of another type, a given scale, queries of very different size, values far from
+    zero (zero points outside the codes' range), peaked scores."""
+    s = Setup(cuda_device, [200, 333], [new, new], 2, 2, 128, 16, "bf16", seed=11, far=3, spread=2.0, shift=6.0)
+    out, lse = omq.kv_attn(*s.args, s.max_q, scale=0.2, out_dtype=torch.float16, lse=True)
+    omq.sync_check()
+    assert out.dtype == torch.float16
+    s.check(out, lse, scale=0.2, rows=11)
+
+
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_missing_pages_hold_no_keys(omq, cuda_device, new):
+    s = Setup(cuda_device, [300, 320, 301], [new, new, new], 2, 1, 64, 32, "f16", seed=13)
+    hidden = [(0, 2), (1, 0), (1, 9), *[(2, p) for p in range(10)]]
+    for (b, p), bad in zip(hidden, [-1, s.pool.shape[0], 2 ** 30, *[-5] * 10]):
+        s.args[2][b, p] = bad
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse, hidden=hidden, rows=17)
+    mine = slice(int(s.cu[2]), int(s.cu[3]))
+    assert not out[mine].any() and bool((lse[mine] == -np.inf).all())
+
+
+@pytest.mark.parametrize("new", [1, 30, 200])
+def test_rows_without_keys_and_rows_behind_the_last(omq, cuda_device, new):
+    """A request with more queries than keys: its first rows see nothing. Rows of q and out
+    behind the last request stay as they were, and a NaN there goes nowhere."""
+    s = Setup(cuda_device, [max(1, new // 2), 90], [new, new], 2, 2, 128, 16, "bf16", seed=17, extra_rows=9)
+    s.lens = s.lens.copy()
+    s.args[0][-9:] = float("nan")
+    out = torch.full_like(s.args[0], 3.0)
+    got, lse = omq.kv_attn(*s.args, s.max_q, out=out, lse=True)
+    omq.sync_check()
+    assert got is out and bool((out[-9:] == 3.0).all())
+    s.check(out[:-9], lse[:-9], rows=7)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_nan_keys_and_values_reach_only_rows_that_see_them(omq, cuda_device, new):
+    s = Setup(cuda_device, [100, 80], [new, min(new, 80)], 1, 2, 128, 16, "f16", seed=19)
+    clean = omq.kv_attn(*s.args, s.max_q)
+    half = kc.CELL * 64
+    for pos, at in ((99, 2 * half), (70, 2 * half + 128)):          # a key step, a value step
+        page, off = divmod(pos, 16)
+        cell = s.pool[s.table[0, page], 0, 0]
+        cell[at + 4 * off: at + 4 * off + 4] = 255
+    out = omq.kv_attn(*s.args, s.max_q)
+    omq.sync_check()
+    first = 70 - (100 - new)                                        # the first row that sees one
+    assert bool(torch.isnan(out[max(first, 0):new]).all())
+    assert torch.equal(out[:max(first, 0)], clean[:max(first, 0)])
+    assert torch.equal(out[new:], clean[new:])
+
+
+def test_strided_queries_and_repeatability(omq, cuda_device):
+    for new in (1, 5, 300):
+        s = Setup(cuda_device, [400, 77, 310], [new, min(new, 77), new], 2, 4, 128, 64, "bf16", seed=23)
+        q = s.args[0]
+        wide = torch.full((q.shape[0], q.shape[1] * 128 + 256), float("nan"), dtype=q.dtype, device=q.device)
+        wide[:, 128:128 + q.shape[1] * 128] = q.flatten(1)
+        view = wide[:, 128:128 + q.shape[1] * 128].unflatten(1, (q.shape[1], 128))
+        want = omq.kv_attn(*s.args, s.max_q)
+        for _ in range(3):
+            assert torch.equal(omq.kv_attn(view, *s.args[1:], s.max_q), want)
+
+
+def test_max_q_cuts_a_request(omq, cuda_device):
+    for new, cut in ((7, 3), (300, 140)):
+        s = Setup(cuda_device, [400, 310], [new, 2], 1, 2, 64, 16, "f16", seed=29)
+        out = torch.full_like(s.args[0], 5.0)
+        omq.kv_attn(*s.args, cut, out=out)
+        assert bool((out[cut:new] == 5.0).all())
+
+
+def test_pool_beyond_32_bit_byte_offsets(omq, cuda_device):
+    page, Hkv = 64, 8
+    n_pages = (5 << 30) // (Hkv * page // 16 * 2304)
+    big = omq.kv_pool(n_pages, Hkv, 128, page, cuda_device)
+    for new in (1, 100):
+        s = Setup(cuda_device, [130, 190], [new, new], Hkv, 1, 128, page, "bf16", seed=31)
+        n = s.pool.shape[0]
+        big[n_pages - n:] = s.pool
+        table = torch.where(s.args[2] >= 0, s.args[2] + (n_pages - n), s.args[2]).int()
+        got = omq.kv_attn(s.args[0], big, table, s.args[3], s.args[4], s.max_q)
+        assert torch.equal(got, omq.kv_attn(*s.args, s.max_q))
