@@ -39,12 +39,12 @@ cudaError_t rows_set_limit(uint64_t ns) {
 
 namespace {
 
-constexpr int W = 4;                  // warps of a block
 constexpr int STEP = 64;              // tokens of a run: four cells
 constexpr int NCELL = STEP / kCell;
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
+constexpr int kMaxSplit = 16;         // blocks of a cluster (above 8 by opt-in)
 
-template <int D, int NB>
+template <int D, int NB, int W>       // W: warps of a block
 struct RowsCfg {
   // cells 16 bytes further apart than they are long: the eight token rows of an ldmatrix come
   // two from each of four cells and fall into eight different 16-byte bank groups (D = 128)
@@ -61,18 +61,36 @@ struct RowsCfg {
   static constexpr int SMEM = BARS + W * STAGES * 8;
 };
 
-__device__ __forceinline__ float load_q(const void* q, int64_t i, omq_dtype dt) {
-  if (dt == OMQ_F16) return __half2float(static_cast<const __half*>(q)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
+// The two 16-bit values of a word.
+__device__ __forceinline__ float2 pair(uint32_t w, bool f16) {
+  if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 dup(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sts128(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+               ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint32_t h2(float a, float b) {
   const __half2 x = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles) {
-  using F = RowsCfg<D, NB>;
+template <int D, int NB, int W>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
+    kv_rows_kernel(AttnParams p, int tiles) {
+  using F = RowsCfg<D, NB, W>;
   using C = CellT<D>;
   constexpr int KM = D / 16;            // K-side matrix steps
   constexpr int VM = D / 16;            // V-side row tiles
@@ -119,75 +137,6 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
   const int vis_max = row_vis(last_row);
   const int n_run = (vis_max + STEP - 1) / STEP;
 
-  // ---- q: this lane's operand values of query row 8 nb + g, its scale and its plain sum
-  uint32_t qf[NB][KM][2];
-  float cq[NB][2], sg[NB][2];           // of the lane's accumulator columns 2 tq, 2 tq + 1
-  int vis[NB][2];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int r = 8 * nb + g;
-    const bool ok = row_ok(r);
-    const int64_t at = ok ? row_at(r) : 0;
-    // the row's largest magnitude: the lane's quarter of the row, then the four lanes
-    float am = 0.f;
-    for (int d = 0; d < D / 4; ++d) {
-      const float x = ok ? fabsf(load_q(p.q, at + tq * (D / 4) + d, p.dt)) : 0.f;
-      am = fmaxf(am, x);
-    }
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    int e = 0;
-    if (am > 0.f && am < INFINITY) e = 14 - ilogbf(am);
-    e = min(max(e, -100), 100);
-    const float up = ldexpf(1.f, e);
-    float sum = 0.f;
-#pragma unroll
-    for (int m = 0; m < KM; ++m) {
-      // matrix step m: word m / 2 of the lane's D / 4 values, nibble pairs (0, 4), (1, 5) or
-      // (2, 6), (3, 7)
-      const int d0 = tq * (D / 4) + 8 * (m >> 1) + 2 * (m & 1);
-      float x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = ok ? load_q(p.q, at + d0 + (j >> 1) + 4 * (j & 1), p.dt) * up : 0.f;
-      // the odd nibbles' codes stand 16 times too high
-      qf[nb][m][0] = h2(x[0], x[1]);
-      qf[nb][m][1] = h2(x[2] * 0.0625f, x[3] * 0.0625f);
-      const float2 u = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][0]));
-      const float2 v = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][1]));
-      sum += (u.x + u.y) + 16.f * (v.x + v.y);
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    // x = h (acc cq - z sg): codes and q carry 2^-24 and 2^e
-    const float down = p.scale * kLog2e * ldexpf(1.f, -e);
-    const float my_cq = down * 16777216.f, my_sg = down * sum;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int src = 4 * (2 * tq + c);                  // a lane with g = 2 tq + c
-      cq[nb][c] = __shfl_sync(0xffffffffu, my_cq, src);
-      sg[nb][c] = __shfl_sync(0xffffffffu, my_sg, src);
-      vis[nb][c] = row_vis(8 * nb + 2 * tq + c);
-    }
-  }
-  const int vis_min = row_vis(0);       // the rows' least (those past the end are not stored)
-
-  float mx[NB][2], ls[NB][2], zs[NB][2];
-  float acc[NB][VM][4];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      mx[nb][c] = -INFINITY;
-      ls[nb][c] = 0.f;
-      zs[nb][c] = 0.f;
-    }
-#pragma unroll
-    for (int m = 0; m < VM; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nb][m][i] = 0.f;
-  }
-
   const uint32_t ring = sb + warp * STAGES * F::STAGE;
   const int nw = cl * W, w0 = rank * W + warp;
   const int32_t* row_table = p.table + static_cast<int64_t>(b) * p.width;
@@ -224,6 +173,77 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
       ++fetched;
     }
   }
+  // ---- q: this lane's operand values of query row 8 nb + g, its scale and its plain sum
+  uint32_t qf[NB][KM][2];
+  float2 cq[NB], sg[NB];                // of the lane's accumulator columns 2 tq, 2 tq + 1
+  int vis[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = 8 * nb + g;
+    const bool ok = row_ok(r), f16 = p.dt == OMQ_F16;
+    // the lane's quarter of the row
+    uint32_t raw[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(
+                               static_cast<const uint16_t*>(p.q) + row_at(r) + tq * (D / 4)) + i)
+                         : make_uint4(0u, 0u, 0u, 0u);
+      raw[4 * i] = u.x; raw[4 * i + 1] = u.y; raw[4 * i + 2] = u.z; raw[4 * i + 3] = u.w;
+    }
+    float am = 0.f;                                      // the row's largest magnitude
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const float2 x = pair(raw[i], f16);
+      am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    int e = 0;
+    if (am > 0.f && am < INFINITY) e = 14 - ilogbf(am);
+    e = min(max(e, -100), 100);
+    const float up = __int_as_float((e + 127) << 23), back = __int_as_float((127 - e) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int m = 0; m < KM; ++m) {
+      // matrix step m: word m / 2 of the lane's codes, nibble pairs (0, 4), (1, 5) or (2, 6),
+      // (3, 7): elements 8 (m / 2) + 2 (m & 1) and the next, and both four further
+      const float2 lo = pair(raw[4 * (m >> 1) + (m & 1)], f16);
+      const float2 hi = pair(raw[4 * (m >> 1) + 2 + (m & 1)], f16);
+      // the odd nibbles' codes stand 16 times too high
+      qf[nb][m][0] = h2(lo.x * up, hi.x * up);
+      qf[nb][m][1] = h2(lo.y * up * 0.0625f, hi.y * up * 0.0625f);
+      const float2 u = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][0]));
+      const float2 v = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][1]));
+      sum += (u.x + u.y) + 16.f * (v.x + v.y);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    // x = h (acc cq + z sg): codes and q carry 2^-24 and 2^e
+    const float down = p.scale * kLog2e * back;
+    const float my_cq = down * 16777216.f, my_sg = -down * sum;
+    const int s0 = 8 * tq, s1 = 8 * tq + 4;              // lanes with g = 2 tq, 2 tq + 1
+    cq[nb].x = __shfl_sync(0xffffffffu, my_cq, s0);
+    cq[nb].y = __shfl_sync(0xffffffffu, my_cq, s1);
+    sg[nb].x = __shfl_sync(0xffffffffu, my_sg, s0);
+    sg[nb].y = __shfl_sync(0xffffffffu, my_sg, s1);
+    vis[nb][0] = row_vis(8 * nb + 2 * tq);
+    vis[nb][1] = row_vis(8 * nb + 2 * tq + 1);
+  }
+  const int vis_min = row_vis(0);       // the rows' least (those past the end are not stored)
+
+  float mx[NB][2];
+  float2 ls[NB], zs[NB];
+  float acc[NB][VM][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    mx[nb][0] = mx[nb][1] = -INFINITY;
+    ls[nb] = zs[nb] = dup(0.f);
+#pragma unroll
+    for (int m = 0; m < VM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nb][m][i] = 0.f;
+  }
+
   bool ok = true;
   int it = 0;
   const int cell_i = g >> 1;                             // the lane's cell in K and P
@@ -257,10 +277,34 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
       const uint32_t cell = st + cell_i * F::PITCH;
       const int t0 = run * STEP + kCell * cell_i + (g & 1);    // + 4 s' + 2 a: the lane's tokens
       const bool cell_ok = (have[s] >> cell_i) & 1u;
-      const bool edge = run * STEP + STEP > vis_min;
+      const bool edge = run * STEP + STEP > vis_min || have[s] != (1u << NCELL) - 1;
 
+      // ---- the run's steps as the lanes need them: (kh, kz, log2 vh, vz) of token
+      // (j, g) = 2 j + (g & 1) of cell g / 2, entry 8 j + g, in place of the cells' steps. A
+      // token that is not there has no weight and finite steps.
+      {
+        float4 mt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int en = lane + 32 * i, ce = (en & 7) >> 1, tok = 2 * (en >> 3) + (en & 1);
+          const uint32_t a = st + ce * F::PITCH + C::KH + 4 * tok;
+          const bool there = ((have[s] >> ce) & 1u) && run * STEP + kCell * ce + tok < vis_max;
+          mt[i].x = there ? lds_f(a) : 0.f;
+          mt[i].y = there ? static_cast<float>(lds_i(a + 64)) : 0.f;
+          mt[i].z = there ? lg2(lds_f(a + 128)) : 0.f;
+          mt[i].w = there ? static_cast<float>(lds_i(a + 192)) : 0.f;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int en = lane + 32 * i;
+          sts128(st + (en >> 4) * F::PITCH + C::KH + (en & 15) * 16, mt[i].x, mt[i].y, mt[i].z,
+                 mt[i].w);
+        }
+        __syncwarp();
+      }
       // ---- scores of the lane's 8 tokens x 2 NB queries
-      float x[NB][8][2];
+      float2 x[NB][8];
 #pragma unroll
       for (int ms = 0; ms < 4; ++ms) {
         float sacc[NB][4];
@@ -293,84 +337,75 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          x[nb][2 * ms][0] = sacc[nb][0];
-          x[nb][2 * ms][1] = sacc[nb][1];
-          x[nb][2 * ms + 1][0] = sacc[nb][2];
-          x[nb][2 * ms + 1][1] = sacc[nb][3];
+          x[nb][2 * ms] = make_float2(sacc[nb][0], sacc[nb][1]);
+          x[nb][2 * ms + 1] = make_float2(sacc[nb][2], sacc[nb][3]);
         }
       }
-      // steps of the lane's tokens; a token that is not there has no weight and a finite step
       float rh[8], vz[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int tok = 2 * j + (g & 1);
-        float kh = lds_f(cell + C::KH + 4 * tok), kz = static_cast<float>(lds_i(cell + C::KZ + 4 * tok));
-        float vh = lds_f(cell + C::VH + 4 * tok);
-        vz[j] = static_cast<float>(lds_i(cell + C::VZ + 4 * tok));
-        const bool there = cell_ok && t0 + 2 * j < vis_max;
-        if (!there) {
-          kh = 0.f;
-          kz = 0.f;
-          vh = 1.f;
-          vz[j] = 0.f;
+        const float4 mt = lds128f(st + (j >> 1) * F::PITCH + C::KH + (j & 1) * 128 + g * 16);
+        // 1 / vh; a NaN step reaches the rows that see the token through lh, and only those
+        rh[j] = mt.z == mt.z ? ex2(-mt.z) : 1.f;
+        vz[j] = mt.w;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float2 t = __ffma2_rn(x[nb][j], cq[nb], __fmul2_rn(dup(mt.y), sg[nb]));
+          x[nb][j] = __ffma2_rn(t, dup(mt.x), dup(mt.z));
         }
-        const float lh = __log2f(vh);
-        // a NaN step reaches the rows that see the token through lh, and only those
-        rh[j] = vh == vh ? __frcp_rn(vh) : 1.f;
+        if (edge) {                                       // warp-uniform
+          const int t = cell_ok ? t0 + 2 * j : 0x7fffffff;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float t = __fmaf_rn(x[nb][j][c], cq[nb][c], -kz * sg[nb][c]);
-            float v = __fmaf_rn(t, kh, lh);
-            if (edge || !cell_ok) v = (there && t0 + 2 * j < vis[nb][c]) ? v : -INFINITY;
-            x[nb][j][c] = v;
+          for (int nb = 0; nb < NB; ++nb) {
+            if (t >= vis[nb][0]) x[nb][j].x = -INFINITY;
+            if (t >= vis[nb][1]) x[nb][j].y = -INFINITY;
           }
+        }
       }
       // ---- running maximum, weights, sums
       uint32_t pw[NB][4][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float al[2];
+        float m0 = x[nb][0].x, m1 = x[nb][0].y;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = x[nb][0][c];
-#pragma unroll
-          for (int j = 1; j < 8; ++j) m = fmaxf(m, x[nb][j][c]);
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          m = fmaxf(m, mx[nb][c]);
-          const float ref = m == -INFINITY ? 0.f : m;
-          al[c] = ex2(mx[nb][c] - ref);
-          mx[nb][c] = m;
-          float l = 0.f, zz = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float w = ex2(x[nb][j][c] - ref);
-            l = __fmaf_rn(w, rh[j], l);
-            x[nb][j][c] = w;
-          }
-          ls[nb][c] = __fmaf_rn(ls[nb][c], al[c], l);
-          // the weights as the matrix instruction takes them
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            zz = __fmaf_rn(__half2float(__float2half_rn(x[nb][j][c])), vz[j], zz);
-          zs[nb][c] = __fmaf_rn(zs[nb][c], al[c], zz);
+        for (int j = 1; j < 8; ++j) {
+          m0 = fmaxf(m0, x[nb][j].x);
+          m1 = fmaxf(m1, x[nb][j].y);
         }
 #pragma unroll
-        for (int ms = 0; ms < 4; ++ms)
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-            pw[nb][ms][a] = movm_t(h2(x[nb][2 * ms + a][0], x[nb][2 * ms + a][1]));
-        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+        for (int o = 4; o < 32; o <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        }
+        m0 = fmaxf(m0, mx[nb][0]);
+        m1 = fmaxf(m1, mx[nb][1]);
+        const float2 ref = make_float2(m0 == -INFINITY ? 0.f : m0, m1 == -INFINITY ? 0.f : m1);
+        const bool moved = m0 != mx[nb][0] || m1 != mx[nb][1];
+        if (__any_sync(0xffffffffu, moved)) {
+          const float2 al = make_float2(ex2(mx[nb][0] - ref.x), ex2(mx[nb][1] - ref.y));
+          mx[nb][0] = m0;
+          mx[nb][1] = m1;
+          ls[nb] = __fmul2_rn(ls[nb], al);
+          zs[nb] = __fmul2_rn(zs[nb], al);
 #pragma unroll
           for (int m = 0; m < VM; ++m) {
-            acc[nb][m][0] *= al[0];
-            acc[nb][m][1] *= al[1];
-            acc[nb][m][2] *= al[0];
-            acc[nb][m][3] *= al[1];
+            acc[nb][m][0] *= al.x;
+            acc[nb][m][1] *= al.y;
+            acc[nb][m][2] *= al.x;
+            acc[nb][m][3] *= al.y;
           }
+        }
+        const float2 nref = make_float2(-ref.x, -ref.y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 y = __fadd2_rn(x[nb][j], nref);
+          const float2 w = make_float2(ex2(y.x), ex2(y.y));
+          ls[nb] = __ffma2_rn(w, dup(rh[j]), ls[nb]);
+          // the weights as the matrix instruction takes them weigh the zero points, too
+          const uint32_t wh = h2(w.x, w.y);
+          zs[nb] = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&wh)), dup(vz[j]),
+                              zs[nb]);
+          pw[nb][j >> 1][j & 1] = movm_t(wh);
         }
       }
       // ---- o^T += V^T w: V's 8 x 8 blocks transposed on their way to registers
@@ -399,7 +434,9 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
           }
         }
       }
-      __syncwarp();                                      // the stage may be written again
+      // the stage may be written again: by the copy engine, after the stores above
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
     }
   }
   if (!ok) {                                             // copies in flight land before the end
@@ -412,19 +449,27 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
 
   // ---- join the warps
   float* stat = reinterpret_cast<float*>(smem + F::STAT);
+  float lsum[NB][2], zsum[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    lsum[nb][0] = ls[nb].x;
+    lsum[nb][1] = ls[nb].y;
+    zsum[nb][0] = zs[nb].x;
+    zsum[nb][1] = zs[nb].y;
+  }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
-        ls[nb][c] += __shfl_xor_sync(0xffffffffu, ls[nb][c], o);
-        zs[nb][c] += __shfl_xor_sync(0xffffffffu, zs[nb][c], o);
+        lsum[nb][c] += __shfl_xor_sync(0xffffffffu, lsum[nb][c], o);
+        zsum[nb][c] += __shfl_xor_sync(0xffffffffu, zsum[nb][c], o);
       }
       if (g == 0) {
         const int r = 8 * nb + 2 * tq + c;
         stat[(0 * W + warp) * F::R + r] = mx[nb][c];
-        stat[(1 * W + warp) * F::R + r] = ls[nb][c];
+        stat[(1 * W + warp) * F::R + r] = lsum[nb][c];
       }
     }
   __syncthreads();                                       // the ring's last readers are done, too
@@ -443,8 +488,8 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
         // row tile q: columns 32 (q / 2) + 4 g + e, e = 2 (q & 1) and the next (16 times high)
         const int d = 32 * (q >> 1) + 4 * g + 2 * (q & 1);
         float2 o;
-        o.x = (acc[nb][q][c] * 16777216.f - zs[nb][c]) * f;
-        o.y = (acc[nb][q][2 + c] * 1048576.f - zs[nb][c]) * f;
+        o.x = (acc[nb][q][c] * 16777216.f - zsum[nb][c]) * f;
+        o.y = (acc[nb][q][2 + c] * 1048576.f - zsum[nb][c]) * f;
         *reinterpret_cast<float2*>(part + (warp * F::R + r) * F::LDO + d) = o;
       }
     }
@@ -514,15 +559,18 @@ __global__ void __launch_bounds__(32 * W) kv_rows_kernel(AttnParams p, int tiles
   if (cl > 1) cluster_sync_all();                        // no block leaves while it is read
 }
 
-template <int D, int NB>
+template <int D, int NB, int W>
 omq_status launch_rows(const AttnParams& p, cudaStream_t st) {
-  using F = RowsCfg<D, NB>;
+  using F = RowsCfg<D, NB, W>;
   static thread_local int ready = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (ready != dev) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_rows_kernel<D, NB>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kv_rows_kernel<D, NB, W>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv_rows_kernel<D, NB, W>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return OMQ_ERR_CUDA;
@@ -535,18 +583,24 @@ omq_status launch_rows(const AttnParams& p, cudaStream_t st) {
   const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
   // split the tokens while there are fewer blocks than the SMs hold and a warp keeps a run
   int cl = 1;
-  while (cl < kMaxCluster && items * cl < 2 * num_sms() && 2 * cl * W <= runs) cl *= 2;
-  launch_cl(kv_rows_kernel<D, NB>, dim3(static_cast<unsigned>(items * cl)), 32 * W, F::SMEM, cl, st,
-            p, static_cast<int>(tiles));
+  while (cl < kMaxSplit && items * cl < 2 * num_sms() && 2 * cl * W <= runs) cl *= 2;
+  launch_cl(kv_rows_kernel<D, NB, W>, dim3(static_cast<unsigned>(items * cl)), 32 * W, F::SMEM, cl,
+            st, p, static_cast<int>(tiles));
   return launch_status();
+}
+
+template <int D>
+omq_status launch_d(const AttnParams& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
+  if (rows > 8) return launch_rows<D, 2, 4>(p, st);
+  if (static_cast<int64_t>(p.n_req) * p.pool.Hkv <= 16) return launch_rows<D, 1, 8>(p, st);
+  return launch_rows<D, 1, 4>(p, st);
 }
 
 }  // namespace
 
 omq_status launch_attn_rows(const AttnParams& p, int64_t D, cudaStream_t st) {
-  const bool one = static_cast<int64_t>(p.max_q) * p.G <= 8;
-  if (D == 128) return one ? launch_rows<128, 1>(p, st) : launch_rows<128, 2>(p, st);
-  return one ? launch_rows<64, 1>(p, st) : launch_rows<64, 2>(p, st);
+  return D == 128 ? launch_d<128>(p, st) : launch_d<64>(p, st);
 }
 
 }  // namespace kv
