@@ -162,7 +162,13 @@ omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_byt
                    static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
                    static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
                    a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
-  return kv::launch_attn_rows(p, a->pool.D, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int kFew = 32;        // query rows per kv head that the row kernel takes
+  const int64_t rows = a->max_q * (a->Hq / a->pool.Hkv);
+  if (rows <= kFew) return kv::launch_attn_rows(p, a->pool.D, kFew, st);
+  if (a->n_req == 1) return kv::launch_attn_tiles(p, a->pool.D, 0, st);
+  KV_TRY(kv::launch_attn_tiles(p, a->pool.D, kFew + 1, st));
+  return kv::launch_attn_rows(p, a->pool.D, kFew, st);
 }
 
 }  // extern "C"

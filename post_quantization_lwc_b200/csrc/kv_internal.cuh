@@ -107,12 +107,17 @@ struct AttnParams {
 omq_status launch_plan(const PlanParams& p, cudaStream_t st);
 omq_status launch_append(const AppendParams& p, int64_t D, cudaStream_t st);
 omq_status launch_read(const ReadParams& p, int64_t D, cudaStream_t st);
-omq_status launch_attn_rows(const AttnParams& p, int64_t D, cudaStream_t st);
+// Attention of the requests with at most max_rows query rows per kv head, 8 or 16 rows a block.
+omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, cudaStream_t st);
+// Attention of the requests with at least min_rows query rows per kv head, 512 rows a CTA pair.
+omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, cudaStream_t st);
 
 // Per translation unit with barrier waits: read and clear its error flag, set its wait limit
 // (the counterparts of take_device_error and set_wait_limit).
 cudaError_t rows_take_error(unsigned* flag);
 cudaError_t rows_set_limit(uint64_t ns);
+cudaError_t tiles_take_error(unsigned* flag);
+cudaError_t tiles_set_limit(uint64_t ns);
 
 // kernel<<<grid, block, smem, stream>>> in clusters of `cluster` blocks along x, with
 // programmatic stream serialization.

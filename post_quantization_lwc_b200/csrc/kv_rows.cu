@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t h2(float a, float b) {
 
 template <int D, int NB, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
-    kv_rows_kernel(AttnParams p, int tiles) {
+    kv_rows_kernel(AttnParams p, int tiles, int max_rows) {
   using F = RowsCfg<D, NB, W>;
   using C = CellT<D>;
   constexpr int KM = D / 16;            // K-side matrix steps
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
   const int n_new = min(max(p.cu[b + 1] - first, 0), p.max_q);
   const int rows = n_new * p.G;
   const int row0 = tile * F::R;
-  if (row0 >= rows || first < 0) return;               // the same for the whole cluster
+  if (row0 >= rows || rows > max_rows || first < 0) return;               // the same for the whole cluster
 
   // row r of the tile: new token (row0 + r) / G, query head kvh G + (row0 + r) mod G; it sees
   // the first vis(r) tokens
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
 }
 
 template <int D, int NB, int W>
-omq_status launch_rows(const AttnParams& p, cudaStream_t st) {
+omq_status launch_rows(const AttnParams& p, int max_rows, cudaStream_t st) {
   using F = RowsCfg<D, NB, W>;
   static thread_local int ready = -1;
   int dev = 0;
@@ -577,30 +577,30 @@ omq_status launch_rows(const AttnParams& p, cudaStream_t st) {
     }
     ready = dev;
   }
-  const int64_t max_rows = static_cast<int64_t>(p.max_q) * p.G;
-  const int64_t tiles = ceil_div(max_rows, F::R);
+  const int64_t most = static_cast<int64_t>(p.max_q) * p.G;
+  const int64_t tiles = ceil_div(most < max_rows ? most : max_rows, F::R);
   const int64_t items = tiles * p.pool.Hkv * p.n_req;
   const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
   // split the tokens while there are fewer blocks than the SMs hold and a warp keeps a run
   int cl = 1;
   while (cl < kMaxSplit && items * cl < 2 * num_sms() && 2 * cl * W <= runs) cl *= 2;
   launch_cl(kv_rows_kernel<D, NB, W>, dim3(static_cast<unsigned>(items * cl)), 32 * W, F::SMEM, cl,
-            st, p, static_cast<int>(tiles));
+            st, p, static_cast<int>(tiles), max_rows);
   return launch_status();
 }
 
 template <int D>
-omq_status launch_d(const AttnParams& p, cudaStream_t st) {
+omq_status launch_d(const AttnParams& p, int max_rows, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-  if (rows > 8) return launch_rows<D, 2, 4>(p, st);
-  if (static_cast<int64_t>(p.n_req) * p.pool.Hkv <= 16) return launch_rows<D, 1, 8>(p, st);
-  return launch_rows<D, 1, 4>(p, st);
+  if (rows > 8) return launch_rows<D, 2, 4>(p, max_rows, st);
+  if (static_cast<int64_t>(p.n_req) * p.pool.Hkv <= 16) return launch_rows<D, 1, 8>(p, max_rows, st);
+  return launch_rows<D, 1, 4>(p, max_rows, st);
 }
 
 }  // namespace
 
-omq_status launch_attn_rows(const AttnParams& p, int64_t D, cudaStream_t st) {
-  return D == 128 ? launch_d<128>(p, st) : launch_d<64>(p, st);
+omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, cudaStream_t st) {
+  return D == 128 ? launch_d<128>(p, max_rows, st) : launch_d<64>(p, max_rows, st);
 }
 
 }  // namespace kv

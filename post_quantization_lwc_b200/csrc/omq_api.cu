@@ -234,6 +234,7 @@ omq_status omq_set_wait_limit_ns(uint64_t ns) {
   if (ns < 1000000ull || ns > 60000000000ull) return OMQ_ERR_SHAPE;
   cudaError_t e = set_wait_limit(ns);
   if (e == cudaSuccess) e = kv::rows_set_limit(ns);
+  if (e == cudaSuccess) e = kv::tiles_set_limit(ns);
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;
@@ -256,10 +257,11 @@ omq_status omq_sync_check(omq_stream_t stream) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;
   }
-  unsigned flag = 0, kv_flag = 0;
+  unsigned flag = 0, rows_flag = 0, tiles_flag = 0;
   e = take_device_error(&flag);
-  if (e == cudaSuccess) e = kv::rows_take_error(&kv_flag);
-  flag |= kv_flag;
+  if (e == cudaSuccess) e = kv::rows_take_error(&rows_flag);
+  if (e == cudaSuccess) e = kv::tiles_take_error(&tiles_flag);
+  flag |= rows_flag | tiles_flag;
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return OMQ_ERR_CUDA;
