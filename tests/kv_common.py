@@ -137,7 +137,7 @@ def get(pool, page, slots, which):
 
 # ------------------------------------------------------------------------------ attention
 
-def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step):
+def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step, operand_half_step=0.0):
     """One query row in binary64 against N keys (codes [N, D], h, z [N, 1]; seen [N] booleans).
     Returns (o, lse, bound of |o|'s error, bound of lse's error).
 
@@ -148,6 +148,8 @@ def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step):
               2^x and log2 h are off by 2^-22 of |x| + |log2 h| + 1 in the exponent
       weights relative change e_p = 2 (max over keys of those) of every p, numerator and sum
       float16 rounding of w = p h, largest 1: relative 2^-11, or 2^-25 absolute
+      operands (many rows) k and v themselves rounded to float16: relative 2^-11 of each and, for
+              k, of scale sum |q| |k| in the score (2^-25 absolute, times 2^-22 of a second part)
       sums    N/16 + 64 float32 additions (the matrix unit's by 2^-22) of terms p h (c + |z|)
       output  half a step of its type."""
     N, D = kc.shape
@@ -167,11 +169,16 @@ def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step):
     mag = (kh * scale * ((kc + np.abs(kz)) @ np.abs(q))[:, None])[:, 0]
     x = np.abs(s) * 1.4427 + np.abs(np.log2(vh[:, 0])) + 1
     e_s = (D + 8) * 2.0 ** -22 * mag.max() + 2.0 ** -21 * x.max()
+    e_s += operand_half_step * (scale * (np.abs((kc - kz) * kh) @ np.abs(q))).max()
+    if operand_half_step:
+        e_s += 2.0 ** -24 * np.abs(q).sum()
     e_p = 2 * e_s
     w = p * vh[:, 0]
     # the largest weight is scaled to 1: absolute float16 error 2^-25 of it
     sub = 2.0 ** -25 * w.max() * (np.abs(vc - vz)).sum(0)
     acc = (n / 16 + 64) * 2.0 ** -22 * (w @ (vc + np.abs(vz)))
-    bound = (2.0 ** -11 + e_p) * (p @ np.abs(v)) + sub + acc
+    bound = (2.0 ** -11 + operand_half_step + e_p) * (p @ np.abs(v)) + sub + acc
+    if operand_half_step:
+        bound = bound + 2.0 ** -24
     bound = bound + out_half_step * (np.abs(o) + bound) + 2.0 ** -25
     return o, lse, bound, e_p + (n / 64 + 64) * 2.0 ** -22 + 2.0 ** -22 * abs(lse)

@@ -86,6 +86,8 @@ class Setup:
         got = out.double().cpu().numpy()
         got_l = None if lse is None else lse.double().cpu().numpy()
         worst = 0.0
+        # a request of more than 32 query rows per kv head takes k and v as float16 operands
+        step = [2.0 ** -11 if n * self.G > 32 else 0.0 for n in self.new]
         for b in range(len(self.lens)):
             n, m = int(self.lens[b]), int(self.new[b])
             there = np.ones(n, bool)
@@ -100,7 +102,7 @@ class Setup:
                     kh = h // self.G
                     (a, ah, az), (c, ch, cz) = self.kv[b]
                     o, l, tol, ltol = kc.attend(self.q[t, h].double().numpy(), a[:, kh], ah[:, kh], az[:, kh],
-                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps)
+                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps, step[b])
                     err = np.abs(got[t, h] - o)
                     assert np.all(err <= tol), (b, i, h, float((err - tol).max()), float(err.max()))
                     worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()))

@@ -64,11 +64,12 @@ class Server:
         got, q = out.double().cpu().numpy(), qt.double().cpu().numpy()
         for t in np.nonzero(req >= 0)[0][::every]:
             mine = self.seen[req[t]]
+            step = 2.0 ** -11 if (req == req[t]).sum() * self.G > 32 else 0.0   # float16 operands
             k, v = ([np.stack([r[i] for r in mine[n][:pos[t] + 1]]) for i in range(3)] for n in ("k", "v"))
             for h in range(0, self.Hkv * self.G, 3):
                 j = h // self.G
                 o, _, tol, _ = kc.attend(q[t, h], *(a[:, j] for a in k), *(a[:, j] for a in v),
-                                         np.ones(pos[t] + 1, bool), self.D ** -0.5, 2.0 ** -11)
+                                         np.ones(pos[t] + 1, bool), self.D ** -0.5, 2.0 ** -11, step)
                 assert np.all(np.abs(got[t, h] - o) <= tol), (t, h)
 
 
