@@ -66,7 +66,7 @@ struct TilesCfg {
                        RAW_OFF = V_OFF + NS * VST, CTL = RAW_OFF + NR * RAW;
   // barriers
   static constexpr int QF = CTL, KF = QF + 16, KE = KF + 8 * NS, VF = KE + 8 * NS,
-                       VE = VF + 8 * NS, SF = VE + 8 * NS, PF = SF + 16, OF = PF + 16,
+                       VE = VF + 8 * NS, SF = VE + 8 * NS, PF = SF + 16, PG = PF + 16, OF = PG + 16,
                        RF = OF + 16, RE = RF + 8 * NR, DR = RE + 8 * NR,
                        // cells that are there per raw stage; cells that are missing per tile
                        MASK = DR + 8, MISS = MASK + 4 * NR, SLOT = MISS + 32, ABORT = SLOT + 4,
@@ -321,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bar_init(sb + F::QF + 8 * s, 8);        // leader's: four warps of either CTA
       bar_init(sb + F::SF + 8 * s, 1);
       bar_init(sb + F::PF + 8 * s, 8);        // leader's
+      bar_init(sb + F::PG + 8 * s, 8);        // leader's
       bar_init(sb + F::OF + 8 * s, 1);
     }
     for (int s = 0; s < NS; ++s) {
@@ -426,45 +427,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         break;
       }
       tc_after();
-      // Two passes over the scores in chunks of 32 columns, rolled loops with the next chunk's
-      // load under way: with all 128 scores in registers the loop body alone was 900
-      // instructions, and the roles' code together missed the instruction cache in 30% of its
-      // requests (827 us against 592 for 8192 tokens of 8 x 4 heads).
-      const int lim = vis - j * KT;
+      // A tile in which some row of the warp hides keys, or whose scores carry a row's power of
+      // two, is put right in tensor memory first (a rolled loop: with this in the unrolled code
+      // the roles' code missed the instruction cache in 30% of its requests, and 8192 tokens of
+      // 8 x 4 heads took 827 us instead of 592).
       const uint32_t gone = miss[j & 7];
-      const bool edge = j * KT + KT > vis_warp || gone != 0;
-      float xa[32], xb[32];
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto take_max = [&](float* x, int c) {
-        if (any_post || edge) {                            // rare: the scores are put back
+      if (any_post || j * KT + KT > vis_warp || gone != 0) {
+        const int lim = vis - j * KT;
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 16) {
+          float x[16];
+          tm_ld16(tS + c, reinterpret_cast<uint32_t*>(x));
+          tm_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const bool hide = c + k >= lim || ((gone >> ((c + k) >> 4)) & 1u);
+          for (int k = 0; k < 16; ++k) {
+            const bool hide = c + k >= lim || ((gone >> (c >> 4)) & 1u);
             x[k] = hide ? -INFINITY : x[k] * post;
           }
           tm_st16(tS + c, reinterpret_cast<uint32_t*>(x));
-          tm_st16(tS + c + 16, reinterpret_cast<uint32_t*>(x + 16));
         }
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], x[k + q], x[k + 4 + q]);
-        }
-      };
-      tm_ld32(tS, reinterpret_cast<uint32_t*>(xa));
-#pragma unroll 1
-      for (int c = 0; c < KT; c += 64) {
-        tm_ld_wait();
-        tm_ld32(tS + c + 32, reinterpret_cast<uint32_t*>(xb));
-        take_max(xa, c);
-        tm_ld_wait();
-        if (c + 64 < KT) tm_ld32(tS + c + 64, reinterpret_cast<uint32_t*>(xa));
-        take_max(xb, c + 32);
+        tm_st_wait();
       }
-      if (any_post || edge) tm_st_wait();
-      // the second pass starts at the front
-      tm_ld32(tS, reinterpret_cast<uint32_t*>(xa));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      float x[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 32) tm_ld32(tS + c, reinterpret_cast<uint32_t*>(x + c));
+      tm_ld_wait();
+      float mx;
+      {
+        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < KT - 4; c += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], x[c + k], x[c + 4 + k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[KT - 4 + k]);
+        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      }
       const bool grow = mx > m + GROW || (m == -INFINITY && mx > -INFINITY);
       if (__any_sync(0xffffffffu, grow)) {
         const float al = grow ? ex2(m - mx) : 1.f;
@@ -492,35 +491,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const float ref = m == -INFINITY ? 0.f : m;
       const float2 nref = make_float2(-ref, -ref);
       float2 la = make_float2(0.f, 0.f), lb = la;
-      auto weigh = [&](float* x, int c) {
-        uint32_t pk[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float2 u = __fadd2_rn(make_float2(x[k], x[k + 1]), nref);
-          const float2 v = __fadd2_rn(make_float2(x[k + 2], x[k + 3]), nref);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const int c = 64 * h + k;
+          const float2 u = __fadd2_rn(make_float2(x[c], x[c + 1]), nref);
+          const float2 v = __fadd2_rn(make_float2(x[c + 2], x[c + 3]), nref);
           const float2 wu = make_float2(ex2(u.x), ex2(u.y)), wv = make_float2(ex2(v.x), ex2(v.y));
           la = __fadd2_rn(la, wu);
           lb = __fadd2_rn(lb, wv);
           pk[k / 2] = pack_h2(wu.x, wu.y);
           pk[k / 2 + 1] = pack_h2(wv.x, wv.y);
         }
-        tm_st16(tS + c / 2, pk);                           // behind the columns still to be read
-      };
-#pragma unroll 1
-      for (int c = 0; c < KT; c += 64) {
-        tm_ld_wait();
-        tm_ld32(tS + c + 32, reinterpret_cast<uint32_t*>(xb));
-        weigh(xa, c);
-        tm_ld_wait();
-        if (c + 64 < KT) tm_ld32(tS + c + 64, reinterpret_cast<uint32_t*>(xa));
-        weigh(xb, c + 32);
+        tm_st16(tS + 32 * h, pk);
+        tm_st16(tS + 32 * h + 16, pk + 16);
+        if (h == 0) {                                      // the first half's product may start
+          tm_st_wait();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) arrive_rank(sb + F::PF + 8 * s, 0);
+        }
       }
       la = __fadd2_rn(la, lb);
       l += la.x + la.y;
       tm_st_wait();
       tc_before();
       __syncwarp();
-      if (lane == 0) arrive_rank(sb + F::PF + 8 * s, 0);
+      if (lane == 0) arrive_rank(sb + F::PG + 8 * s, 0);
     }
     // ---- o
     if (ok && my_nt > 0)
@@ -598,9 +597,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tc_after();
             const uint32_t va = v_lo + st * (F::VST >> 4);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
+            for (int kk = 0; kk < KT / 16; ++kk) {
+              if (kk == KT / 32) {                         // the weights' second half
+                ok = __all_sync(0xffffffffu, wait_for(sb + F::PG + 8 * s, j & 1, abort_flag, DEV_ERR_MMA_WAIT));
+                if (!ok) break;
+                tc_after();
+              }
               mma_ts(leader, 256 + 128 * s, 128 * s + 8 * kk, va + ((kk * 2048) >> 4), id_pv,
                      (j | kk) != 0);
+            }
+            if (!ok) break;
             if (leader) {
               commit_pair(sb + F::OF + 8 * s);
               if (s == 1 || j >= nt1) commit_pair(sb + F::VE + 8 * st);
