@@ -423,35 +423,56 @@ def kv_pool(n_pages, Hkv, D, page, device="cuda") -> torch.Tensor:
                        device=device)
 
 
+def _on(device, stream, entry, args, *rest):
+    """Calls a cache entry point on the tensors' device and on `stream` (default: the device's
+    current one); raises for a status that is not OK. These calls last a few microseconds, so
+    the device is switched only where it is not the current one."""
+    index = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        status = entry(args, *rest, raw)
+    else:
+        with torch.cuda.device(index):
+            status = entry(args, *rest, raw)
+    if status != 0:
+        raise OmqError(status, entry.__name__)
+
+
 def _pool(pool) -> KvPool:
-    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_cuda or not pool.is_contiguous():
+    shape = pool.shape
+    if pool.dtype is not torch.uint8 or len(shape) != 4 or not pool.is_cuda or \
+            not pool.is_contiguous():
         raise ValueError("the pool is a contiguous CUDA uint8 [n_pages, Hkv, page / 16, cell] tensor")
-    n, hkv, cells, cell = pool.shape
+    n, hkv, cells, cell = shape
+    if cell % 16 or kv_cell_bytes((cell - 256) // 16) != cell:
+        raise ValueError("the pool's cells are kv_cell_bytes(D) bytes")
     return KvPool(pool.data_ptr(), n, 16 * cells, hkv, (cell - 256) // 16)
 
 
 def _ints(device, *ts):
     for t in ts:
-        if t is not None and (t.dtype != torch.int32 or t.device != device or
-                              not t.is_contiguous()):
+        if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
             raise ValueError("lengths, tables, slots and positions are contiguous int32 tensors "
                              "on the pool's device")
 
 
-def _rows(device, t, D):
+def _rows(device, t, shape, D):
     """Token stride of a [T, heads, D] tensor whose heads lie back to back."""
-    if t.device != device or t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or \
-            (t.shape[1] > 1 and t.stride(1) != D):
+    if len(shape) != 3 or shape[2] != D or t.device != device:
         raise ValueError("q, k and v are [T, heads, D] CUDA tensors, a token's heads back to back")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    st = t.stride()
+    if st[2] != 1 or (st[1] != D and shape[1] > 1):
+        raise ValueError("q, k and v are [T, heads, D] CUDA tensors, a token's heads back to back")
+    return st[0] if shape[0] > 1 else shape[1] * D
 
 
 def rope_table(n_pos, D, base=10000.0, device="cuda", stream=None) -> torch.Tensor:
     """omq_rope_table: float32 [2, n_pos, D/2], cos and sin of position * base^(-2i/D)."""
     t = torch.empty(2, n_pos, D // 2, dtype=torch.float32, device=device)
-    with torch.cuda.device(t.device):
-        _check(_lib.omq_rope_table(n_pos, D, float(base), _ptr(t), _stream(stream)),
-               "omq_rope_table")
+    _on(t.device, stream, _lib.omq_rope_table, n_pos, D, float(base), t.data_ptr())
     return t
 
 
@@ -465,22 +486,27 @@ def kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_plac
         raise ValueError("tensors must be contiguous CUDA tensors")
     _ints(dev, lens, new_tokens, table, free_pages, n_free)
     B = lens.numel()
-    if table.dim() != 2 or table.shape[0] != B or new_tokens.numel() != B or n_free.numel() != 1:
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B or new_tokens.numel() != B or n_free.numel() != 1:
         raise ValueError("lens and new_tokens are [n_req], table [n_req, width], n_free [1]")
-    own = 0 if in_place else B + 1
+    if capacity < 1:
+        raise OmqError(2, "omq_kv_plan")
     # one allocation: cu, the token maps, and the new lengths
-    buf = torch.empty(B + 1 + 3 * max(capacity, 0) + own, dtype=torch.int32, device=dev)
-    cu, slots, positions, requests, rest = buf.split_with_sizes(
-        [B + 1, capacity, capacity, capacity, own])
-    lens_out, n_free_out = (lens, n_free) if in_place else rest.split_with_sizes([B, 1])
-    a = KvPlanArgs(lens.data_ptr(), new_tokens.data_ptr(), B, table.data_ptr(), table.shape[1],
-                   page, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                   lens_out.data_ptr(), n_free_out.data_ptr(), cu.data_ptr(), slots.data_ptr(),
-                   positions.data_ptr(), requests.data_ptr(), capacity)
-    with torch.cuda.device(dev):
-        _check(_lib.omq_kv_plan(ctypes.byref(a), _stream(stream)), "omq_kv_plan")
-    return dict(lens=lens_out, n_free=n_free_out, cu=cu, slots=slots, positions=positions,
-                requests=requests)
+    own = 0 if in_place else 1
+    buf = torch.empty(B + 1 + 3 * capacity + own * (B + 1), dtype=torch.int32, device=dev)
+    at = buf.data_ptr()
+    maps = at + 4 * (B + 1)
+    after = maps + 12 * capacity
+    a = KvPlanArgs(lens.data_ptr(), new_tokens.data_ptr(), B, table.data_ptr(), shape[1], page,
+                   free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                   after if own else lens.data_ptr(),
+                   after + 4 * B if own else n_free.data_ptr(), at, maps, maps + 4 * capacity,
+                   maps + 8 * capacity, capacity)
+    _on(dev, stream, _lib.omq_kv_plan, ctypes.byref(a))
+    cu, slots, positions, requests, l, f = buf.split_with_sizes(
+        (B + 1, capacity, capacity, capacity, own * B, own))
+    return {"lens": l if own else lens, "n_free": f if own else n_free, "cu": cu, "slots": slots,
+            "positions": positions, "requests": requests}
 
 
 def kv_append(pool, slots, k, v, q=None, positions=None, rope=None, s_a=None, s_o=None,
@@ -488,50 +514,61 @@ def kv_append(pool, slots, k, v, q=None, positions=None, rope=None, s_a=None, s_
     """omq_kv_append: k, v [T, Hkv, D] (token stride free) rotated, scaled, quantized to 4 bits
     and stored at slots [T]. With q [T, Hq, D]: returns q~ [T, Hq, D] (into q_out if given)."""
     P = _pool(pool)
-    dev = pool.device
-    _ints(dev, slots, positions)
+    D, Hkv, dev = P.D, P.Hkv, pool.device
+    _ints(dev, slots)
     T = slots.numel()
-    ld = [0 if t is None else _rows(dev, t, P.D) for t in (q, k, v)]
-    if k.shape[0] != T or v.shape != k.shape or k.shape[1] != P.Hkv or k.dtype != v.dtype or \
-            (q is not None and (q.shape[0] != T or q.dtype != k.dtype)) or \
-            (positions is not None and positions.numel() != T):
-        raise ValueError("q, k, v, slots and positions disagree in tokens, heads or type")
-    for t in (s_a, s_o, delta_o):
-        if t is not None and (t.dtype != torch.float32 or t.device != dev or
-                              not t.is_contiguous() or t.numel() != P.Hkv * P.D):
-            raise ValueError("s_a, s_o and delta_o are contiguous float32 [Hkv, D]")
-    if rope is not None and (rope.dtype != torch.float32 or rope.device != dev or rope.dim() != 3 or
-                             not rope.is_contiguous() or rope.shape[0] != 2 or
-                             rope.shape[2] != P.D // 2):
-        raise ValueError("rope is a contiguous float32 [2, n_pos, D / 2]")
-    if rope is not None and positions is None:
-        raise ValueError("a rotary table needs positions")
-    Hq = 0 if q is None else q.shape[1]
-    if q is not None and q_out is None:
-        q_out = torch.empty(T, Hq, P.D, dtype=q_dtype, device=dev)
-    elif q_out is not None and (q is None or q_out.shape != q.shape or q_out.device != dev or
-                                not q_out.is_contiguous()):
-        raise ValueError("q_out is contiguous, of q's shape")
-    pt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    a = KvAppendArgs(P, T, Hq, _dt(k), pt(q), k.data_ptr(), v.data_ptr(), ld[0], ld[1], ld[2],
-                     slots.data_ptr(), pt(positions), pt(rope), 0 if rope is None else rope.shape[1],
-                     pt(s_a), pt(s_o), pt(delta_o), abits, pt(q_out),
-                     0 if q is None else _dt(q_out))
-    with torch.cuda.device(dev):
-        _check(_lib.omq_kv_append(ctypes.byref(a), _stream(stream)), "omq_kv_append")
+    ks, dt = k.shape, k.dtype
+    k_ld, v_ld = _rows(dev, k, ks, D), _rows(dev, v, v.shape, D)
+    if ks[0] != T or v.shape != ks or ks[1] != Hkv or v.dtype is not dt:
+        raise ValueError("k, v and slots disagree in tokens, heads or type")
+    pos = rp = sa = so = do = qp = qo = None
+    n_pos = Hq = q_ld = qdt = 0
+    if positions is not None:
+        _ints(dev, positions)
+        if positions.numel() != T:
+            raise ValueError("positions are [T]")
+        pos = positions.data_ptr()
+    if rope is not None:
+        rs = rope.shape
+        if pos is None or rope.dtype is not torch.float32 or rope.device != dev or len(rs) != 3 or \
+                rs[0] != 2 or rs[2] != D // 2 or not rope.is_contiguous():
+            raise ValueError("rope is a contiguous float32 [2, n_pos, D / 2], and needs positions")
+        rp, n_pos = rope.data_ptr(), rs[1]
+    if s_a is not None or s_o is not None or delta_o is not None:
+        for t in (s_a, s_o, delta_o):
+            if t is not None and (t.dtype is not torch.float32 or t.device != dev or
+                                  not t.is_contiguous() or t.numel() != Hkv * D):
+                raise ValueError("s_a, s_o and delta_o are contiguous float32 [Hkv, D]")
+        sa, so, do = (None if t is None else t.data_ptr() for t in (s_a, s_o, delta_o))
+    if q is not None:
+        qs = q.shape
+        q_ld, Hq, qp = _rows(dev, q, qs, D), qs[1], q.data_ptr()
+        if qs[0] != T or q.dtype is not dt:
+            raise ValueError("q and k disagree in tokens or type")
+        if q_out is None:
+            q_out = torch.empty(qs, dtype=q_dtype, device=dev)
+        elif q_out.shape != qs or q_out.device != dev or not q_out.is_contiguous():
+            raise ValueError("q_out is contiguous, of q's shape")
+        qo, qdt = q_out.data_ptr(), _dt(q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    a = KvAppendArgs(P, T, Hq, _dt(dt), qp, k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld,
+                     slots.data_ptr(), pos, rp, n_pos, sa, so, do, abits, qo, qdt)
+    _on(dev, stream, _lib.omq_kv_append, ctypes.byref(a))
     return q_out
 
 
 def kv_read(pool, slots, dtype=torch.float32, stream=None):
     """omq_kv_read: the stored (k, v), each [T, Hkv, D], of the slots."""
     P = _pool(pool)
-    _ints(pool.device, slots)
+    dev = pool.device
+    _ints(dev, slots)
     T = slots.numel()
-    k, v = (torch.empty(T, P.Hkv, P.D, dtype=dtype, device=pool.device) for _ in range(2))
-    with torch.cuda.device(pool.device):
-        _check(_lib.omq_kv_read(ctypes.byref(P), T, slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                _dt(k), _stream(stream)), "omq_kv_read")
-    return k, v
+    kv = torch.empty(2, T, P.Hkv, P.D, dtype=dtype, device=dev)
+    at = kv.data_ptr()
+    _on(dev, stream, _lib.omq_kv_read, ctypes.byref(P), T, slots.data_ptr(), at,
+        at + kv.element_size() * T * P.Hkv * P.D, _dt(dtype))
+    return kv.unbind(0)
 
 
 def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, out_dtype=None,
@@ -540,26 +577,26 @@ def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, 
     of a new `out` behind the last request are not written. Returns out [T, Hq, D], or
     (out, lse [T, Hq]) with ``lse``."""
     P = _pool(pool)
-    dev = pool.device
+    dev, D = pool.device, P.D
     _ints(dev, table, lens, cu)
-    ld = _rows(dev, q, P.D)
+    qs, ts = q.shape, table.shape
+    ld = _rows(dev, q, qs, D)
     B = lens.numel()
-    if table.dim() != 2 or table.shape[0] != B or cu.numel() != B + 1:
+    if len(ts) != 2 or ts[0] != B or cu.numel() != B + 1:
         raise ValueError("lens is [n_req], table [n_req, width], cu [n_req + 1]")
-    T, Hq = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(T, Hq, P.D, dtype=out_dtype or q.dtype, device=dev)
-    elif out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        out = torch.empty(qs, dtype=out_dtype or q.dtype, device=dev)
+    elif out.shape != qs or out.device != dev or not out.is_contiguous():
         raise ValueError("out is contiguous, of q's shape")
-    ls = torch.empty(T, Hq, dtype=torch.float32, device=dev) if lse else None
-    a = KvAttnArgs(P, B, T, Hq, q.data_ptr(), ld, _dt(q), table.data_ptr(), table.shape[1],
-                   lens.data_ptr(), cu.data_ptr(), max_q,
-                   P.D ** -0.5 if scale is None else scale, 1 if causal else 0, out.data_ptr(),
-                   _dt(out), None if ls is None else ls.data_ptr())
-    with torch.cuda.device(dev):
-        n = _lib.omq_kv_attn_workspace_bytes(ctypes.byref(a))
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        _check(_lib.omq_kv_attn(ctypes.byref(a), _ptr(ws), n, _stream(stream)), "omq_kv_attn")
+    ls = torch.empty(qs[0], qs[1], dtype=torch.float32, device=dev) if lse else None
+    a = KvAttnArgs(P, B, qs[0], qs[1], q.data_ptr(), ld, _dt(q), table.data_ptr(), ts[1],
+                   lens.data_ptr(), cu.data_ptr(), max_q, D ** -0.5 if scale is None else scale,
+                   1 if causal else 0, out.data_ptr(), _dt(out),
+                   None if ls is None else ls.data_ptr())
+    ref = ctypes.byref(a)
+    n = _lib.omq_kv_attn_workspace_bytes(ref)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _on(dev, stream, _lib.omq_kv_attn, ref, None if ws is None else ws.data_ptr(), n)
     return (out, ls) if lse else out
 
 
