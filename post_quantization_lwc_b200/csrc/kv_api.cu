@@ -56,6 +56,19 @@ omq_status check_attn(const omq_kv_attn_args* a) {
   return OMQ_OK;
 }
 
+// Query rows per kv head up to which a request goes to the row kernel.
+constexpr int kFew = 32;
+
+int64_t most_rows(const omq_kv_attn_args* a) { return a->max_q * (a->Hq / a->pool.Hkv); }
+bool uses_rows(const omq_kv_attn_args* a) { return most_rows(a) <= kFew || a->n_req > 1; }
+
+kv::AttnParams attn_params(const omq_kv_attn_args* a) {
+  return kv::AttnParams{view(a->pool), static_cast<int>(a->n_req), a->T, static_cast<int>(a->Hq),
+                        static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
+                        static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
+                        a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
+}
+
 }  // namespace
 }  // namespace omq
 
@@ -149,26 +162,26 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
 }
 
 size_t omq_kv_attn_workspace_bytes(const omq_kv_attn_args* a) {
-  (void)a;
-  return 0;
+  if (check_attn(a) != OMQ_OK) return 0;
+  const kv::AttnParams p = attn_params(a);
+  return uses_rows(a) ? kv::attn_rows_space(p, a->pool.D, kFew) : 0;
 }
 
 omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_bytes,
                        omq_stream_t stream) {
   KV_TRY(check_attn(a));
-  (void)workspace;
-  (void)ws_bytes;
-  kv::AttnParams p{view(a->pool), static_cast<int>(a->n_req), a->T, static_cast<int>(a->Hq),
-                   static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
-                   static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
-                   a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
+  const kv::AttnParams p = attn_params(a);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  constexpr int kFew = 32;        // query rows per kv head that the row kernel takes
-  const int64_t rows = a->max_q * (a->Hq / a->pool.Hkv);
-  if (rows <= kFew) return kv::launch_attn_rows(p, a->pool.D, kFew, st);
-  if (a->n_req == 1) return kv::launch_attn_tiles(p, a->pool.D, 0, st);
-  KV_TRY(kv::launch_attn_tiles(p, a->pool.D, kFew + 1, st));
-  return kv::launch_attn_rows(p, a->pool.D, kFew, st);
+  if (uses_rows(a)) {
+    const size_t need = kv::attn_rows_space(p, a->pool.D, kFew);
+    if (need && (!workspace || ws_bytes < need)) return OMQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return OMQ_ERR_ALIGN;
+  }
+  // both kernels where the requests differ: each takes those of its kind, by the lengths on
+  // the device
+  if (most_rows(a) > kFew)
+    KV_TRY(kv::launch_attn_tiles(p, a->pool.D, a->n_req == 1 ? 0 : kFew + 1, st));
+  return uses_rows(a) ? kv::launch_attn_rows(p, a->pool.D, kFew, workspace, st) : OMQ_OK;
 }
 
 }  // extern "C"

@@ -108,7 +108,9 @@ omq_status launch_plan(const PlanParams& p, cudaStream_t st);
 omq_status launch_append(const AppendParams& p, int64_t D, cudaStream_t st);
 omq_status launch_read(const ReadParams& p, int64_t D, cudaStream_t st);
 // Attention of the requests with at most max_rows query rows per kv head, 8 or 16 rows a block.
-omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, cudaStream_t st);
+omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, void* space,
+                            cudaStream_t st);
+size_t attn_rows_space(const AttnParams& p, int64_t D, int max_rows);   // bytes of `space`
 // Attention of the requests with at least min_rows query rows per kv head, 512 rows a CTA pair.
 omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, cudaStream_t st);
 

@@ -13,12 +13,16 @@
 // into q (the odd nibbles' q times 1/16; q itself scaled by a power of two per row, so every
 // input type is exact but for values 2^-28 below the row's largest) and into the result.
 //
-// Bound by the cache's bytes: D + 16 per token and kv head. One block per (request, kv head,
-// tile of 8 NB rows) and share of the tokens (a cluster splits them); each warp takes every
-// (blocks x warps)-th run of 64 tokens on its own: a ring of bulk copies (one per 16-token
-// cell, which holds codes and steps together), K as the 16 x 16 operand straight from 16-byte
-// shared loads, V transposed by ldmatrix, no barrier between warps until the end. Warps, then
-// blocks (through the cluster's shared memory) join their (max, sum, o) in a fixed order.
+// Bound by the cache's bytes: D + 16 per token and kv head. The work is a line of runs of 64
+// tokens, item after item (an item: request, tile of 8 NB rows, kv head), cut into equal parts,
+// one a block, whatever the lengths: one block per item left the SMs 30% to 80% busy on 64
+// ragged contexts of up to 8192 tokens, and a cluster per item was slower for many items and
+// reached only 128 SMs for few. Within a part each of the block's four warps takes every fourth
+// run on its own: a ring of bulk copies (one per 16-token cell, which holds codes and steps
+// together), K as the 16 x 16 operand straight from 16-byte shared loads, V transposed by
+// ldmatrix, no barrier between warps. At the end of an item or part the warps join their (max,
+// sum, o) in a fixed order; an item cut between blocks leaves float32 partials in the workspace,
+// which a second kernel joins in the blocks' order.
 #include "kv_internal.cuh"
 
 namespace omq {
@@ -42,9 +46,9 @@ namespace {
 constexpr int STEP = 64;              // tokens of a run: four cells
 constexpr int NCELL = STEP / kCell;
 constexpr int STAGES = 2;
-constexpr int kMaxSplit = 16;         // blocks of a cluster (above 8 by opt-in)
+constexpr int W = 4;                  // warps of a block
 
-template <int D, int NB, int W>       // W: warps of a block
+template <int D, int NB>
 struct RowsCfg {
   // cells 16 bytes further apart than they are long: the eight token rows of an ldmatrix come
   // two from each of four cells and fall into eight different 16-byte bank groups (D = 128)
@@ -55,10 +59,26 @@ struct RowsCfg {
   static constexpr int LDO = D + 4;                     // row stride of the partial outputs
   static constexpr int PART = W * R * LDO * 4;          // the warps' partial outputs (ring reused)
   static constexpr int BODY = RING > PART ? RING : PART;
-  static constexpr int STAT = BODY;                     // float [3][W][R]: max, sum, z sum
-  static constexpr int JOIN = STAT + 3 * W * R * 4;     // float [R][2] the block's (max, sum)
+  static constexpr int STAT = BODY;                     // float [2][W][R]: max, sum
+  static constexpr int JOIN = STAT + 2 * W * R * 4;     // float [R][2] the block's (max, sum)
   static constexpr int BARS = JOIN + R * 8;             // mbarriers [W][STAGES]
-  static constexpr int SMEM = BARS + W * STAGES * 8;
+  static constexpr int SCAN = BARS + W * STAGES * 8;     // int64 [W], then the part's start
+  static constexpr int SMEM = SCAN + W * 8 + 16;
+};
+
+// The workspace of a cut launch: per block its first and last item's partial o [2][R][D] and
+// (max, sum) [2][R][2], and what of the item its first run continues the second kernel needs.
+struct PartDesc {
+  int joins;            // the item ends here: this block's number joins it
+  int b, tile, kvh;
+  int first;            // the block it starts in
+  int first_slot;       // that block's slot of it
+  int pad[2];
+};
+struct RowsSpace {
+  float* o;
+  float2* ml;
+  PartDesc* desc;
 };
 
 // The two 16-bit values of a word.
@@ -82,15 +102,90 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Of a word of codes, per 16-bit lane: the low byte (16 c1 + c0) 2^-24 and c0 2^-24, and the same
+// of the high byte. Four operations of the half-rate logic pipe (the masks and shifts are what
+// this kernel issues most); 16 c1 is the difference, on the FMA pipe.
+struct Nibbles {
+  uint32_t u0, l0, u1, l1;
+};
+__device__ __forceinline__ Nibbles nibbles(uint32_t w) {
+  Nibbles n;
+  n.u0 = w & 0x00FF00FFu;
+  n.l0 = w & 0x000F000Fu;
+  n.u1 = __byte_perm(w, 0u, 0x4341);
+  n.l1 = n.u1 & 0x000F000Fu;
+  return n;
+}
 __device__ __forceinline__ uint32_t h2(float a, float b) {
   const __half2 x = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-template <int D, int NB, int W>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
-    kv_rows_kernel(AttnParams p, int tiles, int max_rows) {
-  using F = RowsCfg<D, NB, W>;
+// Two values of an output row from their unnormalised sums, its maximum m and sum l; the first
+// column's thread also writes the row's log-sum-exp.
+__device__ __forceinline__ void store_row(const AttnParams& p, int64_t orow, int D, int d, float2 o,
+                                          float m, float l) {
+  const bool none = l == 0.f;                            // a visible key adds 1 / hv, or NaN
+  const float inv = none ? 0.f : 1.f / l;
+  const float yx = none ? 0.f : o.x * inv, yy = none ? 0.f : o.y * inv;
+  uint32_t packed;
+  if (p.out_dt == OMQ_F16) {
+    packed = h2(yx, yy);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(yx, yy);
+    packed = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = packed;
+  if (p.lse && d == 0) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
+}
+
+// Query rows of a request, and its runs per item (one without keys still writes its zeros).
+struct ReqWork {
+  int len, first, n_new, rows, tiles, runs;
+};
+template <int R>
+__device__ __forceinline__ ReqWork req_work(const AttnParams& p, int b, int max_rows) {
+  ReqWork r;
+  r.len = min(max(__ldg(p.lens + b), 0), p.width * p.pool.page);
+  r.first = __ldg(p.cu + b);
+  r.n_new = min(max(__ldg(p.cu + b + 1) - r.first, 0), p.max_q);
+  r.rows = r.n_new * p.G;
+  r.tiles = r.rows > max_rows || r.first < 0 ? 0 : (r.rows + R - 1) / R;
+  r.runs = max(1, (r.len + STEP - 1) / STEP);
+  return r;
+}
+// Inclusive prefix sum over the block, and its total.
+__device__ __forceinline__ int64_t scan_block(int64_t v, volatile int64_t* sm, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) sm[w] = v;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    before += i < w ? sm[i] : 0;
+    all += sm[i];
+  }
+  *total = all;
+  return v + before;
+}
+
+// cut: the blocks share the line of runs evenly; else block i takes item i whole (tiles per
+// request and head as the host bounds them).
+template <int D, int NB>
+__global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
+    kv_rows_kernel(AttnParams p, int tiles, int max_rows, int cut, RowsSpace ws) {
+  using F = RowsCfg<D, NB>;
   using C = CellT<D>;
   constexpr int KM = D / 16;            // K-side matrix steps
   constexpr int VM = D / 16;            // V-side row tiles
@@ -99,11 +194,6 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
   const uint32_t sb = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
-  const int cl = static_cast<int>(cta_count()), rank = static_cast<int>(cta_rank());
-  const int item = blockIdx.x / cl;
-  const int tile = item % tiles;
-  const int kvh = (item / tiles) % p.pool.Hkv;
-  const int b = item / tiles / p.pool.Hkv;
   const uint32_t bars = sb + F::BARS + warp * STAGES * 8;
   if (lane == 0) {
     for (int s = 0; s < STAGES; ++s) bar_init(bars + 8 * s, 1);
@@ -113,13 +203,76 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
   pdl_wait();
   pdl_launch();
 
-  const int room = p.width * p.pool.page;
-  const int len = min(max(p.lens[b], 0), room);
-  const int first = p.cu[b];
-  const int n_new = min(max(p.cu[b + 1] - first, 0), p.max_q);
-  const int rows = n_new * p.G;
+  // ---- this block's part of the line: [at, end) in request b, which starts at base
+  int b = 0, bt = 0;
+  int64_t base = 0, at = 0, end = 0, part = 0;
+  if (cut) {
+    volatile int64_t* sm = reinterpret_cast<volatile int64_t*>(smem + F::SCAN);
+    int64_t total = 0, sum;
+    int64_t incl = 0, mine = 0;
+    for (int c = 0; c < p.n_req; c += 32 * W) {
+      mine = 0;
+      if (c + static_cast<int>(threadIdx.x) < p.n_req) {
+        const ReqWork r = req_work<F::R>(p, c + threadIdx.x, max_rows);
+        mine = static_cast<int64_t>(r.tiles) * p.pool.Hkv * r.runs;
+      }
+      incl = total + scan_block(mine, sm, &sum);
+      total += sum;
+    }
+    if (threadIdx.x == 0) ws.desc[blockIdx.x].joins = 0;
+    // at least a run a warp
+    part = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(W));
+    at = part * blockIdx.x;
+    end = min(at + part, total);
+    if (at >= end) return;
+    int64_t done = 0;
+    for (int c = 0; c < p.n_req; c += 32 * W) {
+      if (p.n_req > 32 * W) {                              // else the sums above are these
+        mine = 0;
+        if (c + static_cast<int>(threadIdx.x) < p.n_req) {
+          const ReqWork r = req_work<F::R>(p, c + threadIdx.x, max_rows);
+          mine = static_cast<int64_t>(r.tiles) * p.pool.Hkv * r.runs;
+        }
+        incl = done + scan_block(mine, sm, &sum);
+        done += sum;
+      }
+      if (at < incl && at >= incl - mine) {
+        sm[W] = incl - mine;
+        reinterpret_cast<volatile int*>(sm + W + 1)[0] = c + threadIdx.x;
+      }
+      if (p.n_req > 32 * W && done > at) break;            // the same for the whole block
+    }
+    __syncthreads();
+    base = sm[W];
+    b = reinterpret_cast<volatile int*>(sm + W + 1)[0];
+  } else {
+    const int item = blockIdx.x;
+    bt = item % tiles * p.pool.Hkv + (item / tiles) % p.pool.Hkv;
+    b = item / tiles / p.pool.Hkv;
+  }
+
+  uint32_t it = 0;                       // runs this warp has taken: its ring position
+  int seg = 0;
+  bool ok = true;
+  for (; cut ? at < end : seg == 0; ++seg) {
+  const ReqWork rw = req_work<F::R>(p, b, max_rows);
+  int run0 = 0, run1 = rw.runs;
+  if (cut) {
+    const int64_t off = at - base;
+    if (off >= static_cast<int64_t>(rw.tiles) * p.pool.Hkv * rw.runs) {   // the next request
+      base += static_cast<int64_t>(rw.tiles) * p.pool.Hkv * rw.runs;
+      ++b;
+      --seg;
+      continue;
+    }
+    bt = static_cast<int>(off / rw.runs);
+    run0 = static_cast<int>(off - static_cast<int64_t>(bt) * rw.runs);
+    run1 = static_cast<int>(min(static_cast<int64_t>(rw.runs), run0 + (end - at)));
+  }
+  const int tile = bt / p.pool.Hkv, kvh = bt - tile * p.pool.Hkv;
+  const int len = rw.len, first = rw.first, n_new = rw.n_new, rows = rw.rows;
   const int row0 = tile * F::R;
-  if (row0 >= rows || rows > max_rows || first < 0) return;               // the same for the whole cluster
+  if (!cut && tile >= rw.tiles) return;
 
   // row r of the tile: new token (row0 + r) / G, query head kvh G + (row0 + r) mod G; it sees
   // the first vis(r) tokens
@@ -135,10 +288,10 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
   };
   const int last_row = min(F::R, rows - row0) - 1;
   const int vis_max = row_vis(last_row);
-  const int n_run = (vis_max + STEP - 1) / STEP;
+  const int n_run = ok ? min(run1, (vis_max + STEP - 1) / STEP) : 0;
 
   const uint32_t ring = sb + warp * STAGES * F::STAGE;
-  const int nw = cl * W, w0 = rank * W + warp;
+  const int w0 = run0 + warp;
   const int32_t* row_table = p.table + static_cast<int64_t>(b) * p.width;
   const int n_cell = (vis_max + kCell - 1) / kCell;
   // Copies run `run` into stage s; returns which of its four cells exist (bit i: cell i).
@@ -163,16 +316,16 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
     return mask;
   };
 
-  uint32_t have[STAGES];
+  uint32_t have = 0;                     // four bits a stage: its cells that are there
   int fetched = 0;
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) {
-    have[s] = 0;
-    if (s < STAGES - 1 && w0 + s * nw < n_run) {
-      have[s] = fetch(w0 + s * nw, s);
+  for (int k = 0; k < STAGES - 1; ++k)
+    if (w0 + k * W < n_run) {
+      const uint32_t st = (it + k) % STAGES;
+      have |= fetch(w0 + k * W, st) << (4 * st);
       ++fetched;
     }
-  }
+
   // ---- q: this lane's operand values of query row 8 nb + g, its scale and its plain sum
   uint32_t qf[NB][KM][2];
   float2 cq[NB], sg[NB];                // of the lane's accumulator columns 2 tq, 2 tq + 1
@@ -244,21 +397,16 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
       for (int i = 0; i < 4; ++i) acc[nb][m][i] = 0.f;
   }
 
-  bool ok = true;
-  int it = 0;
   const int cell_i = g >> 1;                             // the lane's cell in K and P
-  for (int run = w0; run < n_run && ok; run += nw) {
-    // one stage per unrolled step, so that have[] stays in registers
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) {
-      if (run >= n_run) break;
-      if (s) {
-        run += nw;
-        if (run >= n_run) break;
-      }
-      const int ahead = run + (STAGES - 1) * nw;
+  int taken = 0;
+#pragma unroll 1
+  for (int run = w0; run < n_run && ok; run += W) {
+    {
+      const uint32_t s = it % STAGES;
+      const int ahead = run + (STAGES - 1) * W;
       if (ahead < n_run) {
-        have[(s + STAGES - 1) % STAGES] = fetch(ahead, (s + STAGES - 1) % STAGES);
+        const uint32_t st = (it + STAGES - 1) % STAGES;
+        have = (have & ~(15u << (4 * st))) | (fetch(ahead, st) << (4 * st));
         ++fetched;
       }
       int got = 0;
@@ -273,11 +421,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
         break;
       }
       ++it;
+      ++taken;
+      const uint32_t cells = (have >> (4 * s)) & 15u;
       const uint32_t st = ring + s * F::STAGE;
       const uint32_t cell = st + cell_i * F::PITCH;
       const int t0 = run * STEP + kCell * cell_i + (g & 1);    // + 4 s' + 2 a: the lane's tokens
-      const bool cell_ok = (have[s] >> cell_i) & 1u;
-      const bool edge = run * STEP + STEP > vis_min || have[s] != (1u << NCELL) - 1;
+      const bool cell_ok = (cells >> cell_i) & 1u;
+      const bool edge = run * STEP + STEP > vis_min || cells != (1u << NCELL) - 1;
 
       // ---- the run's steps as the lanes need them: (kh, kz, log2 vh, vz) of token
       // (j, g) = 2 j + (g & 1) of cell g / 2, entry 8 j + g, in place of the cells' steps. A
@@ -288,7 +438,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
         for (int i = 0; i < 2; ++i) {
           const int en = lane + 32 * i, ce = (en & 7) >> 1, tok = 2 * (en >> 3) + (en & 1);
           const uint32_t a = st + ce * F::PITCH + C::KH + 4 * tok;
-          const bool there = ((have[s] >> ce) & 1u) && run * STEP + kCell * ce + tok < vis_max;
+          const bool there = ((cells >> ce) & 1u) && run * STEP + kCell * ce + tok < vis_max;
           mt[i].x = there ? lds_f(a) : 0.f;
           mt[i].y = there ? static_cast<float>(lds_i(a + 64)) : 0.f;
           mt[i].z = there ? lg2(lds_f(a + 128)) : 0.f;
@@ -326,13 +476,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+          const Nibbles a = nibbles(wa[w]), b2 = nibbles(wb[w]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            mma16816(sacc[nb], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u,
-                     wb[w] & 0x00F000F0u, qf[nb][2 * w][0], qf[nb][2 * w][1]);
-            mma16816(sacc[nb], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
-                     b8 & 0x00F000F0u, qf[nb][2 * w + 1][0], qf[nb][2 * w + 1][1]);
+            mma16816(sacc[nb], a.l0, b2.l0, hsub2(a.u0, a.l0), hsub2(b2.u0, b2.l0),
+                     qf[nb][2 * w][0], qf[nb][2 * w][1]);
+            mma16816(sacc[nb], a.l1, b2.l1, hsub2(a.u1, a.l1), hsub2(b2.u1, b2.l1),
+                     qf[nb][2 * w + 1][0], qf[nb][2 * w + 1][1]);
           }
         }
 #pragma unroll
@@ -421,15 +571,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
           ldsm4_t(va, v);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const uint32_t lo = v[2 * q], hi = v[2 * q + 1];
-            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+            // the second row is the whole byte, 16 c' + c: c's sum comes off at the end
+            const Nibbles lo = nibbles(v[2 * q]), hi = nibbles(v[2 * q + 1]);
             const int m = 2 * (2 * jj + q);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              mma16816(acc[nb][m], lo & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x000F000Fu,
-                       hi & 0x00F000F0u, pw[nb][ms][0], pw[nb][ms][1]);
-              mma16816(acc[nb][m + 1], lo8 & 0x000F000Fu, lo8 & 0x00F000F0u, hi8 & 0x000F000Fu,
-                       hi8 & 0x00F000F0u, pw[nb][ms][0], pw[nb][ms][1]);
+              mma16816(acc[nb][m], lo.l0, lo.u0, hi.l0, hi.u0, pw[nb][ms][0], pw[nb][ms][1]);
+              mma16816(acc[nb][m + 1], lo.l1, lo.u1, hi.l1, hi.u1, pw[nb][ms][0], pw[nb][ms][1]);
             }
           }
         }
@@ -439,13 +587,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
       __syncwarp();
     }
   }
-  if (!ok) {                                             // copies in flight land before the end
-    if (lane == 0)
-      for (int j = it; j < fetched; ++j)
-        bar_wait(bars + 8 * (j % STAGES), (j / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
-                 DEV_ERR_TMA_WAIT);
-    __syncwarp();
+  if (!ok && lane == 0) {                                // copies in flight land before the end
+    const uint32_t t0 = it - taken;
+    for (uint32_t j = it; j < t0 + fetched; ++j)
+      bar_wait(bars + 8 * (j % STAGES), (j / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
+               DEV_ERR_TMA_WAIT);
   }
+  __syncwarp();
 
   // ---- join the warps
   float* stat = reinterpret_cast<float*>(smem + F::STAT);
@@ -473,7 +621,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
       }
     }
   __syncthreads();                                       // the ring's last readers are done, too
-  float* part = reinterpret_cast<float*>(smem);          // [W][R][LDO]
+  float* part_o = reinterpret_cast<float*>(smem);        // [W][R][LDO]
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -489,8 +637,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
         const int d = 32 * (q >> 1) + 4 * g + 2 * (q & 1);
         float2 o;
         o.x = (acc[nb][q][c] * 16777216.f - zsum[nb][c]) * f;
-        o.y = (acc[nb][q][2 + c] * 1048576.f - zsum[nb][c]) * f;
-        *reinterpret_cast<float2*>(part + (warp * F::R + r) * F::LDO + d) = o;
+        o.y = ((acc[nb][q][2 + c] - acc[nb][q][c]) * 1048576.f - zsum[nb][c]) * f;
+        *reinterpret_cast<float2*>(part_o + (warp * F::R + r) * F::LDO + d) = o;
       }
     }
   __syncthreads();
@@ -512,95 +660,188 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 1 : NB == 1 ? 3 : 2)
   }
   for (int i = threadIdx.x; i < F::R * (D / 2); i += 32 * W) {
     const int r = i / (D / 2), d = 2 * (i % (D / 2));
-    float2 s = *reinterpret_cast<float2*>(part + r * F::LDO + d);
+    float2 s = *reinterpret_cast<float2*>(part_o + r * F::LDO + d);
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-      const float2 u = *reinterpret_cast<float2*>(part + (w * F::R + r) * F::LDO + d);
+      const float2 u = *reinterpret_cast<float2*>(part_o + (w * F::R + r) * F::LDO + d);
       s.x += u.x;
       s.y += u.y;
     }
-    *reinterpret_cast<float2*>(part + r * F::LDO + d) = s;
+    *reinterpret_cast<float2*>(part_o + r * F::LDO + d) = s;
   }
-  // ---- join the cluster's blocks: each finishes its share of the tile's values
-  if (cl > 1) cluster_sync_all();
-  else __syncthreads();
-  const int n_val = F::R * (D / 2), share = (n_val + cl - 1) / cl;
-  const int hi = min(n_val, (rank + 1) * share);
-  for (int i = rank * share + static_cast<int>(threadIdx.x); i < hi; i += 32 * W) {
+  __syncthreads();
+  const bool whole = run0 == 0 && run1 == rw.runs;
+  const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg > 0 ? 1 : 0);
+  if (!whole) {
+    if (threadIdx.x < F::R) ws.ml[slot * F::R + threadIdx.x] = make_float2(join[2 * threadIdx.x], join[2 * threadIdx.x + 1]);
+    if (threadIdx.x == 0 && seg == 0 && run0 > 0 && run1 == rw.runs) {
+      const int64_t start = at - run0;
+      PartDesc d;
+      d.joins = 1;
+      d.b = b; d.tile = tile; d.kvh = kvh;
+      d.first = static_cast<int>(start / part);
+      d.first_slot = start == d.first * part ? 0 : 1;
+      ws.desc[blockIdx.x] = d;
+    }
+  }
+  for (int i = threadIdx.x; i < F::R * (D / 2); i += 32 * W) {
     const int r = i / (D / 2), d = 2 * (i % (D / 2));
-    if (!row_ok(r)) continue;
-    const uint32_t ja = sb + F::JOIN + 8 * r, pa = sb + (r * F::LDO + d) * 4;
-    float m = -INFINITY;
-    for (int k = 0; k < cl; ++k) m = fmaxf(m, ld_cluster(map_rank(ja, k)));
-    float l = 0.f, ox = 0.f, oy = 0.f;
-    for (int k = 0; k < cl; ++k) {
-      const float2 ml = ld_cluster2(map_rank(ja, k));
-      const float2 o = ld_cluster2(map_rank(pa, k));
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-      l = __fmaf_rn(ml.y, f, l);
-      ox = __fmaf_rn(o.x, f, ox);
-      oy = __fmaf_rn(o.y, f, oy);
+    const float2 o = *reinterpret_cast<const float2*>(part_o + r * F::LDO + d);
+    if (!whole) {
+      *reinterpret_cast<float2*>(ws.o + (slot * F::R + r) * D + d) = o;
+    } else if (row_ok(r)) {
+      const int tok = (row0 + r) / p.G;
+      const int64_t orow = static_cast<int64_t>(first + tok) * p.Hq + kvh * p.G + (row0 + r) - tok * p.G;
+      store_row(p, orow, D, d, o, join[2 * r], join[2 * r + 1]);
     }
-    const bool none = l == 0.f;                          // a visible key adds 1 / hv or NaN
-    const float inv = none ? 0.f : 1.f / l;
-    const float yx = none ? 0.f : ox * inv, yy = none ? 0.f : oy * inv;
-    const int tok = (row0 + r) / p.G;
-    const int64_t orow = static_cast<int64_t>(first + tok) * p.Hq + kvh * p.G + (row0 + r) - tok * p.G;
-    uint32_t packed;
-    if (p.out_dt == OMQ_F16) packed = h2(yx, yy);
-    else {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(yx, yy);
-      packed = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = packed;
-    if (p.lse && d == 0)
-      p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
   }
-  if (cl > 1) cluster_sync_all();                        // no block leaves while it is read
+  // the ring may be filled again: by the copy engine, after the stores above
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  at += run1 - run0;
+  }
 }
 
-template <int D, int NB, int W>
-omq_status launch_rows(const AttnParams& p, int max_rows, cudaStream_t st) {
-  using F = RowsCfg<D, NB, W>;
+// One row of an item that was cut: blockIdx.x the block it ends in, blockIdx.y the row of the
+// tile. The partials are joined in the blocks' order (two interleaved halves, then their sum).
+template <int D, int NB>
+__global__ void __launch_bounds__(128) kv_rows_join_kernel(AttnParams p, int max_rows, RowsSpace ws) {
+  constexpr int R = 8 * NB;
+  constexpr int HALVES = 128 / (D / 2);
+  __shared__ float2 half_sum[HALVES - 1][D / 2];
+  __shared__ float red[4];
+  __shared__ float fac[128];
+  pdl_wait();
+  pdl_launch();
+  const PartDesc d = ws.desc[blockIdx.x];
+  if (!d.joins) return;
+  const int r = blockIdx.y;
+  const ReqWork rw = req_work<R>(p, d.b, max_rows);
+  const int row = d.tile * R + r;
+  if (row >= rw.rows || rw.first + row / p.G >= p.T) return;
+  const int n = static_cast<int>(blockIdx.x) - d.first + 1;
+  auto slot_of = [&](int i) { return (2 * static_cast<int64_t>(d.first + i) + (i == 0 ? d.first_slot : 0)) * R + r; };
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += 128) m = fmaxf(m, ws.ml[slot_of(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const int h = threadIdx.x / (D / 2), v = threadIdx.x % (D / 2);
+  float l = 0.f;
+  float2 o = make_float2(0.f, 0.f);
+  for (int c = 0; c < n; c += 128) {
+    __syncthreads();
+    float mine = 0.f;
+    if (c + static_cast<int>(threadIdx.x) < n) {
+      const float2 ml = ws.ml[slot_of(c + threadIdx.x)];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+      fac[threadIdx.x] = f;
+      mine = ml.y * f;                                     // 0, or NaN where a key was NaN
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, k);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    l += (red[0] + red[1]) + (red[2] + red[3]);
+    const int hi = min(n - c, 128);
+#pragma unroll 8
+    for (int i = h; i < hi; i += HALVES) {
+      const float2 u = *reinterpret_cast<const float2*>(ws.o + slot_of(c + i) * D + 2 * v);
+      o.x = __fmaf_rn(u.x, fac[i], o.x);
+      o.y = __fmaf_rn(u.y, fac[i], o.y);
+    }
+  }
+  if (h > 0) half_sum[h - 1][v] = o;
+  __syncthreads();
+  if (h > 0) return;
+#pragma unroll
+  for (int k = 0; k < HALVES - 1; ++k) {
+    o.x += half_sum[k][v].x;
+    o.y += half_sum[k][v].y;
+  }
+  const int tok = row / p.G;
+  const int64_t orow = static_cast<int64_t>(rw.first + tok) * p.Hq + d.kvh * p.G + row - tok * p.G;
+  store_row(p, orow, D, 2 * v, o, m, l);
+}
+
+// How a launch is laid out; the workspace depends on it.
+struct RowsPlan {
+  int64_t tiles;
+  int64_t blocks;
+  bool cut;
+};
+template <int D, int NB>
+RowsPlan plan_rows(const AttnParams& p, int max_rows) {
+  const int64_t most = static_cast<int64_t>(p.max_q) * p.G;
+  RowsPlan r;
+  r.tiles = ceil_div(most < max_rows ? most : max_rows, 8 * NB);
+  const int64_t items = r.tiles * p.pool.Hkv * p.n_req;
+  const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
+  const int64_t room = (NB == 1 ? 3 : 2) * static_cast<int64_t>(num_sms());
+  // whole items where a block's four warps have at most two runs each, or the blocks fill the
+  // SMs many times over (and a long item is a small part of the whole)
+  r.cut = runs > 2 * W && items < 8 * room;
+  const int64_t parts = ceil_div(items * runs, W);
+  r.blocks = !r.cut ? items : parts < room ? parts : room;
+  return r;
+}
+template <int D, int NB>
+size_t space_of(const RowsPlan& r, void* base, RowsSpace* ws) {
+  if (!r.cut) return 0;
+  constexpr int R = 8 * NB;
+  const size_t o = static_cast<size_t>(r.blocks) * 2 * R * D * 4, ml = static_cast<size_t>(r.blocks) * 2 * R * 8;
+  if (ws) {
+    ws->o = static_cast<float*>(base);
+    ws->ml = reinterpret_cast<float2*>(static_cast<char*>(base) + o);
+    ws->desc = reinterpret_cast<PartDesc*>(static_cast<char*>(base) + o + ml);
+  }
+  return o + ml + static_cast<size_t>(r.blocks) * sizeof(PartDesc);
+}
+
+template <int D, int NB>
+omq_status launch_rows(const AttnParams& p, int max_rows, void* space, cudaStream_t st) {
+  using F = RowsCfg<D, NB>;
   static thread_local int ready = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (ready != dev) {
-    cudaError_t e = cudaFuncSetAttribute(kv_rows_kernel<D, NB, W>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv_rows_kernel<D, NB, W>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(kv_rows_kernel<D, NB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return OMQ_ERR_CUDA;
     }
     ready = dev;
   }
-  const int64_t most = static_cast<int64_t>(p.max_q) * p.G;
-  const int64_t tiles = ceil_div(most < max_rows ? most : max_rows, F::R);
-  const int64_t items = tiles * p.pool.Hkv * p.n_req;
-  const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
-  // split the tokens while there are fewer blocks than the SMs hold and a warp keeps a run
-  int cl = 1;
-  while (cl < kMaxSplit && items * cl < 2 * num_sms() && 2 * cl * W <= runs) cl *= 2;
-  launch_cl(kv_rows_kernel<D, NB, W>, dim3(static_cast<unsigned>(items * cl)), 32 * W, F::SMEM, cl,
-            st, p, static_cast<int>(tiles), max_rows);
+  const RowsPlan r = plan_rows<D, NB>(p, max_rows);
+  RowsSpace ws = {};
+  space_of<D, NB>(r, space, &ws);
+  launch_k(kv_rows_kernel<D, NB>, dim3(static_cast<unsigned>(r.blocks)), 32 * W, F::SMEM, st, p,
+           static_cast<int>(r.tiles), max_rows, r.cut ? 1 : 0, ws);
+  const omq_status s = launch_status();
+  if (s != OMQ_OK || !r.cut) return s;
+  launch_k(kv_rows_join_kernel<D, NB>, dim3(static_cast<unsigned>(r.blocks), 8 * NB), 128, 0, st, p, max_rows, ws);
   return launch_status();
 }
 
-template <int D>
-omq_status launch_d(const AttnParams& p, int max_rows, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-  if (rows > 8) return launch_rows<D, 2, 4>(p, max_rows, st);
-  if (static_cast<int64_t>(p.n_req) * p.pool.Hkv <= 16) return launch_rows<D, 1, 8>(p, max_rows, st);
-  return launch_rows<D, 1, 4>(p, max_rows, st);
-}
+bool one_tile(const AttnParams& p) { return static_cast<int64_t>(p.max_q) * p.G <= 8; }
 
 }  // namespace
 
-omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, cudaStream_t st) {
-  return D == 128 ? launch_d<128>(p, max_rows, st) : launch_d<64>(p, max_rows, st);
+size_t attn_rows_space(const AttnParams& p, int64_t D, int max_rows) {
+  if (D == 128)
+    return one_tile(p) ? space_of<128, 1>(plan_rows<128, 1>(p, max_rows), nullptr, nullptr)
+                       : space_of<128, 2>(plan_rows<128, 2>(p, max_rows), nullptr, nullptr);
+  return one_tile(p) ? space_of<64, 1>(plan_rows<64, 1>(p, max_rows), nullptr, nullptr)
+                     : space_of<64, 2>(plan_rows<64, 2>(p, max_rows), nullptr, nullptr);
+}
+
+omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, void* space, cudaStream_t st) {
+  if (D == 128)
+    return one_tile(p) ? launch_rows<128, 1>(p, max_rows, space, st) : launch_rows<128, 2>(p, max_rows, space, st);
+  return one_tile(p) ? launch_rows<64, 1>(p, max_rows, space, st) : launch_rows<64, 2>(p, max_rows, space, st);
 }
 
 }  // namespace kv
