@@ -21,8 +21,13 @@ omq_status check_pool(const omq_kv_pool& p) {
   return OMQ_OK;
 }
 kv::Pool view(const omq_kv_pool& p) {
-  return kv::Pool{static_cast<uint8_t*>(p.data), p.n_pages, static_cast<int>(p.Hkv),
-                  static_cast<int>(p.page / 16), static_cast<int>(p.page)};
+  const int cells = static_cast<int>(p.page / 16);
+  int shift = -1;
+  if ((cells & (cells - 1)) == 0)
+    for (shift = 0; (1 << shift) < cells; ++shift) {
+    }
+  return kv::Pool{static_cast<uint8_t*>(p.data), p.n_pages, static_cast<int>(p.Hkv), cells,
+                  static_cast<int>(p.page), shift};
 }
 // Rows of `heads` heads, `ld` elements apart, each 16-byte aligned.
 omq_status check_rows(const void* p, int64_t ld, int64_t heads, int64_t D, omq_dtype dt) {

@@ -33,6 +33,7 @@ struct Pool {
   int Hkv;
   int cells;        // cells per page (page / 16)
   int page;
+  int shift;        // log2 of cells where it is a power of two, else -1
 };
 
 struct PlanParams {

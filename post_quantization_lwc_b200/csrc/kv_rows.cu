@@ -10,8 +10,8 @@
 // float16 (the operand; the same rounded value weighs zv_j) is relative to the largest
 // contribution. A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
 // second nibble of a 16-bit lane: one AND makes two operands, exact, and the powers of two go
-// into q (the odd nibbles' q times 1/16; q itself scaled by a power of two per row, so every
-// input type is exact but for values 2^-28 below the row's largest) and into the result.
+// into q (the odd nibbles' q times 1/16; the tile's q scaled by a power of two, so both input
+// types are exact but for values 2^-28 below the tile's largest) and into the result.
 //
 // Bound by the cache's bytes: D + 16 per token and kv head. The work is a line of runs of 64
 // tokens, item after item (an item: request, tile of 8 NB rows, kv head), cut into equal parts,
@@ -86,7 +86,11 @@ __device__ __forceinline__ float2 pair(uint32_t w, bool f16) {
   if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ float2 dup(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -300,7 +304,8 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     int id = -1;
     uint32_t pg = 0;
     if (lane < NCELL && ci < n_cell) {
-      pg = static_cast<uint32_t>(ci) / static_cast<uint32_t>(p.pool.cells);
+      pg = p.pool.shift >= 0 ? static_cast<uint32_t>(ci) >> p.pool.shift
+                             : static_cast<uint32_t>(ci) / static_cast<uint32_t>(p.pool.cells);
       id = row_table[pg];
     }
     const bool have = id >= 0 && id < p.pool.n_pages;
@@ -328,69 +333,74 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
 
   // ---- q: this lane's operand values of query row 8 nb + g, its scale and its plain sum
   uint32_t qf[NB][KM][2];
-  float2 cq[NB], sg[NB];                // of the lane's accumulator columns 2 tq, 2 tq + 1
+  float sg[NB][2];                      // of the lane's accumulator columns 2 tq, 2 tq + 1
   int vis[NB][2];
+  float cq;                             // what the products' powers of two and the scale come to
+  {
+    const bool f16 = p.dt == OMQ_F16;
+    uint32_t raw[NB][D / 8];            // the lane's quarter of the row
+    float am = 0.f;                     // the tile's largest magnitude
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int r = 8 * nb + g;
-    const bool ok = row_ok(r), f16 = p.dt == OMQ_F16;
-    // the lane's quarter of the row
-    uint32_t raw[D / 8];
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + g;
+      const bool here = row_ok(r);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(
-                               static_cast<const uint16_t*>(p.q) + row_at(r) + tq * (D / 4)) + i)
-                         : make_uint4(0u, 0u, 0u, 0u);
-      raw[4 * i] = u.x; raw[4 * i + 1] = u.y; raw[4 * i + 2] = u.z; raw[4 * i + 3] = u.w;
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 u = here ? __ldg(reinterpret_cast<const uint4*>(
+                                   static_cast<const uint16_t*>(p.q) + row_at(r) + tq * (D / 4)) + i)
+                             : make_uint4(0u, 0u, 0u, 0u);
+        raw[nb][4 * i] = u.x; raw[nb][4 * i + 1] = u.y;
+        raw[nb][4 * i + 2] = u.z; raw[nb][4 * i + 3] = u.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 x = pair(raw[nb][i], f16);
+        am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
     }
-    float am = 0.f;                                      // the row's largest magnitude
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const float2 x = pair(raw[i], f16);
-      am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
-    }
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
     int e = 0;
     if (am > 0.f && am < INFINITY) e = 14 - ilogbf(am);
     e = min(max(e, -100), 100);
     const float up = __int_as_float((e + 127) << 23), back = __int_as_float((127 - e) << 23);
-    float sum = 0.f;
-#pragma unroll
-    for (int m = 0; m < KM; ++m) {
-      // matrix step m: word m / 2 of the lane's codes, nibble pairs (0, 4), (1, 5) or (2, 6),
-      // (3, 7): elements 8 (m / 2) + 2 (m & 1) and the next, and both four further
-      const float2 lo = pair(raw[4 * (m >> 1) + (m & 1)], f16);
-      const float2 hi = pair(raw[4 * (m >> 1) + 2 + (m & 1)], f16);
-      // the odd nibbles' codes stand 16 times too high
-      qf[nb][m][0] = h2(lo.x * up, hi.x * up);
-      qf[nb][m][1] = h2(lo.y * up * 0.0625f, hi.y * up * 0.0625f);
-      const float2 u = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][0]));
-      const float2 v = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][1]));
-      sum += (u.x + u.y) + 16.f * (v.x + v.y);
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    // x = h (acc cq + z sg): codes and q carry 2^-24 and 2^e
+    // x = h (acc cq + z sg) + log2 hv: codes and q carry 2^-24 and 2^e
     const float down = p.scale * kLog2e * back;
-    const float my_cq = down * 16777216.f, my_sg = -down * sum;
-    const int s0 = 8 * tq, s1 = 8 * tq + 4;              // lanes with g = 2 tq, 2 tq + 1
-    cq[nb].x = __shfl_sync(0xffffffffu, my_cq, s0);
-    cq[nb].y = __shfl_sync(0xffffffffu, my_cq, s1);
-    sg[nb].x = __shfl_sync(0xffffffffu, my_sg, s0);
-    sg[nb].y = __shfl_sync(0xffffffffu, my_sg, s1);
-    vis[nb][0] = row_vis(8 * nb + 2 * tq);
-    vis[nb][1] = row_vis(8 * nb + 2 * tq + 1);
+    cq = down * 16777216.f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        // matrix step m: word m / 2 of the lane's codes, nibble pairs (0, 4), (1, 5) or (2, 6),
+        // (3, 7): elements 8 (m / 2) + 2 (m & 1) and the next, and both four further
+        const float2 lo = pair(raw[nb][4 * (m >> 1) + (m & 1)], f16);
+        const float2 hi = pair(raw[nb][4 * (m >> 1) + 2 + (m & 1)], f16);
+        // the odd nibbles' codes stand 16 times too high
+        qf[nb][m][0] = h2(lo.x * up, hi.x * up);
+        qf[nb][m][1] = h2(lo.y * up * 0.0625f, hi.y * up * 0.0625f);
+        const float2 u = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][0]));
+        const float2 v = __half22float2(*reinterpret_cast<__half2*>(&qf[nb][m][1]));
+        sum += (u.x + u.y) + 16.f * (v.x + v.y);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float my_sg = -down * sum;
+      sg[nb][0] = __shfl_sync(0xffffffffu, my_sg, 8 * tq);       // lanes with g = 2 tq, 2 tq + 1
+      sg[nb][1] = __shfl_sync(0xffffffffu, my_sg, 8 * tq + 4);
+      vis[nb][0] = row_vis(8 * nb + 2 * tq);
+      vis[nb][1] = row_vis(8 * nb + 2 * tq + 1);
+    }
   }
   const int vis_min = row_vis(0);       // the rows' least (those past the end are not stored)
 
   float mx[NB][2];
-  float2 ls[NB], zs[NB];
+  float ls[NB][2], zs[NB][2];
   float acc[NB][VM][4];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     mx[nb][0] = mx[nb][1] = -INFINITY;
-    ls[nb] = zs[nb] = dup(0.f);
+    ls[nb][0] = ls[nb][1] = zs[nb][0] = zs[nb][1] = 0.f;
 #pragma unroll
     for (int m = 0; m < VM; ++m)
 #pragma unroll
@@ -429,9 +439,10 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
       const bool cell_ok = (cells >> cell_i) & 1u;
       const bool edge = run * STEP + STEP > vis_min || cells != (1u << NCELL) - 1;
 
-      // ---- the run's steps as the lanes need them: (kh, kz, log2 vh, vz) of token
+      // ---- the run's steps as the lanes need them: (kh cq, kh kz, log2 vh, vz) of token
       // (j, g) = 2 j + (g & 1) of cell g / 2, entry 8 j + g, in place of the cells' steps. A
-      // token that is not there has no weight and finite steps.
+      // token that is not there has no weight and finite steps; a NaN step of V is put into K's,
+      // so that it reaches the rows that see the token, and only those.
       {
         float4 mt[2];
 #pragma unroll
@@ -439,9 +450,12 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           const int en = lane + 32 * i, ce = (en & 7) >> 1, tok = 2 * (en >> 3) + (en & 1);
           const uint32_t a = st + ce * F::PITCH + C::KH + 4 * tok;
           const bool there = ((cells >> ce) & 1u) && run * STEP + kCell * ce + tok < vis_max;
-          mt[i].x = there ? lds_f(a) : 0.f;
-          mt[i].y = there ? static_cast<float>(lds_i(a + 64)) : 0.f;
-          mt[i].z = there ? lg2(lds_f(a + 128)) : 0.f;
+          const float kh = there ? lds_f(a) : 0.f, kz = there ? static_cast<float>(lds_i(a + 64)) : 0.f;
+          const float vh = there ? lds_f(a + 128) : 1.f;
+          const bool bad = vh != vh;
+          mt[i].x = bad ? NAN : kh * cq;
+          mt[i].y = kh * kz;
+          mt[i].z = bad ? 0.f : lg2(vh);
           mt[i].w = there ? static_cast<float>(lds_i(a + 192)) : 0.f;
         }
         __syncwarp();
@@ -491,17 +505,16 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           x[nb][2 * ms + 1] = make_float2(sacc[nb][2], sacc[nb][3]);
         }
       }
-      float rh[8], vz[8];
+      float lh[8], vz[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float4 mt = lds128f(st + (j >> 1) * F::PITCH + C::KH + (j & 1) * 128 + g * 16);
-        // 1 / vh; a NaN step reaches the rows that see the token through lh, and only those
-        rh[j] = mt.z == mt.z ? ex2(-mt.z) : 1.f;
+        lh[j] = mt.z;
         vz[j] = mt.w;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float2 t = __ffma2_rn(x[nb][j], cq[nb], __fmul2_rn(dup(mt.y), sg[nb]));
-          x[nb][j] = __ffma2_rn(t, dup(mt.x), dup(mt.z));
+          x[nb][j].x = __fmaf_rn(x[nb][j].x, mt.x, __fmaf_rn(mt.y, sg[nb][0], mt.z));
+          x[nb][j].y = __fmaf_rn(x[nb][j].y, mt.x, __fmaf_rn(mt.y, sg[nb][1], mt.z));
         }
         if (edge) {                                       // warp-uniform
           const int t = cell_ok ? t0 + 2 * j : 0x7fffffff;
@@ -516,12 +529,14 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
       uint32_t pw[NB][4][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float m0 = x[nb][0].x, m1 = x[nb][0].y;
+        float m0 = max3(x[nb][0].x, x[nb][1].x, x[nb][2].x), m1 = max3(x[nb][0].y, x[nb][1].y, x[nb][2].y);
 #pragma unroll
-        for (int j = 1; j < 8; ++j) {
-          m0 = fmaxf(m0, x[nb][j].x);
-          m1 = fmaxf(m1, x[nb][j].y);
+        for (int j = 3; j < 7; j += 2) {
+          m0 = max3(m0, x[nb][j].x, x[nb][j + 1].x);
+          m1 = max3(m1, x[nb][j].y, x[nb][j + 1].y);
         }
+        m0 = fmaxf(m0, x[nb][7].x);
+        m1 = fmaxf(m1, x[nb][7].y);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
@@ -529,32 +544,35 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
         }
         m0 = fmaxf(m0, mx[nb][0]);
         m1 = fmaxf(m1, mx[nb][1]);
-        const float2 ref = make_float2(m0 == -INFINITY ? 0.f : m0, m1 == -INFINITY ? 0.f : m1);
+        const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
         const bool moved = m0 != mx[nb][0] || m1 != mx[nb][1];
         if (__any_sync(0xffffffffu, moved)) {
-          const float2 al = make_float2(ex2(mx[nb][0] - ref.x), ex2(mx[nb][1] - ref.y));
+          const float al0 = ex2(mx[nb][0] - ref0), al1 = ex2(mx[nb][1] - ref1);
           mx[nb][0] = m0;
           mx[nb][1] = m1;
-          ls[nb] = __fmul2_rn(ls[nb], al);
-          zs[nb] = __fmul2_rn(zs[nb], al);
+          ls[nb][0] *= al0;
+          ls[nb][1] *= al1;
+          zs[nb][0] *= al0;
+          zs[nb][1] *= al1;
 #pragma unroll
           for (int m = 0; m < VM; ++m) {
-            acc[nb][m][0] *= al.x;
-            acc[nb][m][1] *= al.y;
-            acc[nb][m][2] *= al.x;
-            acc[nb][m][3] *= al.y;
+            acc[nb][m][0] *= al0;
+            acc[nb][m][1] *= al1;
+            acc[nb][m][2] *= al0;
+            acc[nb][m][3] *= al1;
           }
         }
-        const float2 nref = make_float2(-ref.x, -ref.y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 y = __fadd2_rn(x[nb][j], nref);
-          const float2 w = make_float2(ex2(y.x), ex2(y.y));
-          ls[nb] = __ffma2_rn(w, dup(rh[j]), ls[nb]);
+          const float w0 = ex2(x[nb][j].x - ref0), w1 = ex2(x[nb][j].y - ref1);
+          const float rh = ex2(-lh[j]);                    // 1 / vh
+          ls[nb][0] = __fmaf_rn(w0, rh, ls[nb][0]);
+          ls[nb][1] = __fmaf_rn(w1, rh, ls[nb][1]);
           // the weights as the matrix instruction takes them weigh the zero points, too
-          const uint32_t wh = h2(w.x, w.y);
-          zs[nb] = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&wh)), dup(vz[j]),
-                              zs[nb]);
+          const uint32_t wh = h2(w0, w1);
+          const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&wh));
+          zs[nb][0] = __fmaf_rn(wr.x, vz[j], zs[nb][0]);
+          zs[nb][1] = __fmaf_rn(wr.y, vz[j], zs[nb][1]);
           pw[nb][j >> 1][j & 1] = movm_t(wh);
         }
       }
@@ -600,10 +618,10 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
   float lsum[NB][2], zsum[NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    lsum[nb][0] = ls[nb].x;
-    lsum[nb][1] = ls[nb].y;
-    zsum[nb][0] = zs[nb].x;
-    zsum[nb][1] = zs[nb].y;
+    lsum[nb][0] = ls[nb][0];
+    lsum[nb][1] = ls[nb][1];
+    zsum[nb][0] = zs[nb][0];
+    zsum[nb][1] = zs[nb][1];
   }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
