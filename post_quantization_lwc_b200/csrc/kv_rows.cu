@@ -70,10 +70,13 @@ struct RowsCfg {
 // (max, sum) [2][R][2], and what of the item its first run continues the second kernel needs.
 struct PartDesc {
   int joins;            // the item ends here: this block's number joins it
-  int b, tile, kvh;
+  int row0;             // its first query row: token row0 / G of the request
+  int rows;             // its query rows that are stored
+  int tok0;             // the request's first row of q and out
+  int kvh;
   int first;            // the block it starts in
   int first_slot;       // that block's slot of it
-  int pad[2];
+  int pad;
 };
 struct RowsSpace {
   float* o;
@@ -184,11 +187,12 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, volatile int64_t* sm, i
   return v + before;
 }
 
-// cut: the blocks share the line of runs evenly; else block i takes item i whole (tiles per
-// request and head as the host bounds them).
+// pieces == 0: the blocks share the line of runs evenly. pieces > 0: an item has that many
+// blocks, each an equal share of its runs, at least one a warp (1: block i takes item i whole);
+// tiles per request and head as the host bounds them.
 template <int D, int NB>
 __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
-    kv_rows_kernel(AttnParams p, int tiles, int max_rows, int cut, RowsSpace ws) {
+    kv_rows_kernel(AttnParams p, int tiles, int max_rows, int pieces, RowsSpace ws) {
   using F = RowsCfg<D, NB>;
   using C = CellT<D>;
   constexpr int KM = D / 16;            // K-side matrix steps
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
   // ---- this block's part of the line: [at, end) in request b, which starts at base
   int b = 0, bt = 0;
   int64_t base = 0, at = 0, end = 0, part = 0;
+  const bool cut = pieces == 0;
   if (cut) {
     volatile int64_t* sm = reinterpret_cast<volatile int64_t*>(smem + F::SCAN);
     int64_t total = 0, sum;
@@ -250,7 +255,8 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     base = sm[W];
     b = reinterpret_cast<volatile int*>(sm + W + 1)[0];
   } else {
-    const int item = blockIdx.x;
+    const int item = blockIdx.x / pieces;
+    if (pieces > 1 && threadIdx.x == 0) ws.desc[blockIdx.x].joins = 0;
     bt = item % tiles * p.pool.Hkv + (item / tiles) % p.pool.Hkv;
     b = item / tiles / p.pool.Hkv;
   }
@@ -272,6 +278,11 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     bt = static_cast<int>(off / rw.runs);
     run0 = static_cast<int>(off - static_cast<int64_t>(bt) * rw.runs);
     run1 = static_cast<int>(min(static_cast<int64_t>(rw.runs), run0 + (end - at)));
+  } else if (pieces > 1) {
+    const int share = max((rw.runs + pieces - 1) / pieces, W);
+    run0 = static_cast<int>(blockIdx.x) % pieces * share;
+    run1 = min(run0 + share, rw.runs);
+    if (run0 >= rw.runs) return;
   }
   const int tile = bt / p.pool.Hkv, kvh = bt - tile * p.pool.Hkv;
   const int len = rw.len, first = rw.first, n_new = rw.n_new, rows = rw.rows;
@@ -694,11 +705,18 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     if (threadIdx.x < F::R) ws.ml[slot * F::R + threadIdx.x] = make_float2(join[2 * threadIdx.x], join[2 * threadIdx.x + 1]);
     if (threadIdx.x == 0 && seg == 0 && run0 > 0 && run1 == rw.runs) {
       const int64_t start = at - run0;
-      PartDesc d;
+      PartDesc d = {};
       d.joins = 1;
-      d.b = b; d.tile = tile; d.kvh = kvh;
-      d.first = static_cast<int>(start / part);
-      d.first_slot = start == d.first * part ? 0 : 1;
+      d.row0 = row0;
+      d.rows = min(F::R, rows - row0);
+      d.tok0 = first;
+      d.kvh = kvh;
+      if (cut) {
+        d.first = static_cast<int>(start / part);
+        d.first_slot = start == d.first * part ? 0 : 1;
+      } else {
+        d.first = static_cast<int>(blockIdx.x) / pieces * pieces;
+      }
       ws.desc[blockIdx.x] = d;
     }
   }
@@ -721,66 +739,85 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
 }
 
 // One row of an item that was cut: blockIdx.x the block it ends in, blockIdx.y the row of the
-// tile. The partials are joined in the blocks' order (two interleaved halves, then their sum).
+// tile. The partials are joined in the blocks' order (interleaved halves or quarters, then their
+// sum). Everything is latency here: a thread has its first four partials under way before it
+// knows the maxima.
 template <int D, int NB>
-__global__ void __launch_bounds__(128) kv_rows_join_kernel(AttnParams p, int max_rows, RowsSpace ws) {
-  constexpr int R = 8 * NB;
-  constexpr int HALVES = 128 / (D / 2);
-  __shared__ float2 half_sum[HALVES - 1][D / 2];
-  __shared__ float red[4];
+__global__ void __launch_bounds__(128) kv_rows_join_kernel(AttnParams p, RowsSpace ws) {
+  constexpr int R = 8 * NB, TPR = D / 2, GRP = 128 / TPR, AHEAD = 4;
+  __shared__ float2 grp_sum[GRP - 1][TPR];
+  __shared__ float red[2][4];
   __shared__ float fac[128];
   pdl_wait();
   pdl_launch();
   const PartDesc d = ws.desc[blockIdx.x];
-  if (!d.joins) return;
   const int r = blockIdx.y;
-  const ReqWork rw = req_work<R>(p, d.b, max_rows);
-  const int row = d.tile * R + r;
-  if (row >= rw.rows || rw.first + row / p.G >= p.T) return;
+  if (!d.joins || r >= d.rows) return;
+  const int row = d.row0 + r, tok = d.tok0 + row / p.G;
+  if (tok >= p.T) return;
   const int n = static_cast<int>(blockIdx.x) - d.first + 1;
-  auto slot_of = [&](int i) { return (2 * static_cast<int64_t>(d.first + i) + (i == 0 ? d.first_slot : 0)) * R + r; };
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += 128) m = fmaxf(m, ws.ml[slot_of(i)].x);
+  auto slot_of = [&](int i) {
+    return (2 * static_cast<int64_t>(d.first + i) + (i == 0 ? d.first_slot : 0)) * R + r;
+  };
+  const int h = threadIdx.x / TPR, v = threadIdx.x % TPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (static_cast<int>(threadIdx.x) < n) ml = ws.ml[slot_of(threadIdx.x)];
+  float2 u[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const int i = h + k * GRP;
+    u[k] = i < n ? *reinterpret_cast<const float2*>(ws.o + slot_of(i) * D + 2 * v) : make_float2(0.f, 0.f);
+  }
+  float m = ml.x;
+  for (int i = threadIdx.x + 128; i < n; i += 128) m = fmaxf(m, ws.ml[slot_of(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  if (lane == 0) red[0][warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const int h = threadIdx.x / (D / 2), v = threadIdx.x % (D / 2);
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   float l = 0.f;
   float2 o = make_float2(0.f, 0.f);
   for (int c = 0; c < n; c += 128) {
-    __syncthreads();
-    float mine = 0.f;
-    if (c + static_cast<int>(threadIdx.x) < n) {
-      const float2 ml = ws.ml[slot_of(c + threadIdx.x)];
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-      fac[threadIdx.x] = f;
-      mine = ml.y * f;                                     // 0, or NaN where a key was NaN
+    if (c) {
+      __syncthreads();                                     // the last chunk's factors are read
+      ml = make_float2(-INFINITY, 0.f);
+      if (c + static_cast<int>(threadIdx.x) < n) ml = ws.ml[slot_of(c + threadIdx.x)];
     }
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+    fac[threadIdx.x] = f;
+    float mine = ml.y * f;                                 // 0, or NaN where a key was NaN
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, k);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mine;
+    if (lane == 0) red[1][warp] = mine;
     __syncthreads();
-    l += (red[0] + red[1]) + (red[2] + red[3]);
+    l += (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
     const int hi = min(n - c, 128);
+    int i = h;
+    if (c == 0) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k, i += GRP)
+        if (i < hi) {
+          o.x = __fmaf_rn(u[k].x, fac[i], o.x);
+          o.y = __fmaf_rn(u[k].y, fac[i], o.y);
+        }
+    }
 #pragma unroll 8
-    for (int i = h; i < hi; i += HALVES) {
-      const float2 u = *reinterpret_cast<const float2*>(ws.o + slot_of(c + i) * D + 2 * v);
-      o.x = __fmaf_rn(u.x, fac[i], o.x);
-      o.y = __fmaf_rn(u.y, fac[i], o.y);
+    for (; i < hi; i += GRP) {
+      const float2 w = *reinterpret_cast<const float2*>(ws.o + slot_of(c + i) * D + 2 * v);
+      o.x = __fmaf_rn(w.x, fac[i], o.x);
+      o.y = __fmaf_rn(w.y, fac[i], o.y);
     }
   }
-  if (h > 0) half_sum[h - 1][v] = o;
+  if (h > 0) grp_sum[h - 1][v] = o;
   __syncthreads();
   if (h > 0) return;
 #pragma unroll
-  for (int k = 0; k < HALVES - 1; ++k) {
-    o.x += half_sum[k][v].x;
-    o.y += half_sum[k][v].y;
+  for (int k = 0; k < GRP - 1; ++k) {
+    o.x += grp_sum[k][v].x;
+    o.y += grp_sum[k][v].y;
   }
-  const int tok = row / p.G;
-  const int64_t orow = static_cast<int64_t>(rw.first + tok) * p.Hq + d.kvh * p.G + row - tok * p.G;
+  const int64_t orow = static_cast<int64_t>(tok) * p.Hq + d.kvh * p.G + row - row / p.G * p.G;
   store_row(p, orow, D, 2 * v, o, m, l);
 }
 
@@ -788,7 +825,7 @@ __global__ void __launch_bounds__(128) kv_rows_join_kernel(AttnParams p, int max
 struct RowsPlan {
   int64_t tiles;
   int64_t blocks;
-  bool cut;
+  int pieces;          // blocks of an item, 0: the line of runs is cut evenly
 };
 template <int D, int NB>
 RowsPlan plan_rows(const AttnParams& p, int max_rows) {
@@ -798,16 +835,33 @@ RowsPlan plan_rows(const AttnParams& p, int max_rows) {
   const int64_t items = r.tiles * p.pool.Hkv * p.n_req;
   const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
   const int64_t room = (NB == 1 ? 3 : 2) * static_cast<int64_t>(num_sms());
-  // whole items where a block's four warps have at most two runs each, or the blocks fill the
-  // SMs many times over (and a long item is a small part of the whole)
-  r.cut = runs > 2 * W && items < 8 * room;
+  // whole items where a block's four warps have at most two runs each, or where the blocks fill
+  // the SMs many times over (a long item is then a small part of the whole)
+  if (runs <= 2 * W || items >= 8 * room) {
+    r.pieces = 1;
+    r.blocks = items;
+    return r;
+  }
+  // Equal shares of each item while all blocks are resident at once, if the requests are as long
+  // as each other (there is one) or the shares short; no block then handles two items, which
+  // costs it a second round of latencies (one request of 2049 tokens, 32 heads: 10.9 us against
+  // 15.7). Else the even line.
+  int64_t pieces = room / items;
+  const int64_t useful = ceil_div(runs, W);
+  if (pieces > useful) pieces = useful;
+  if (pieces > 1 && (p.n_req == 1 || ceil_div(runs, pieces) <= 4 * W)) {
+    r.pieces = static_cast<int>(pieces);
+    r.blocks = items * pieces;
+    return r;
+  }
   const int64_t parts = ceil_div(items * runs, W);
-  r.blocks = !r.cut ? items : parts < room ? parts : room;
+  r.pieces = 0;
+  r.blocks = parts < room ? parts : room;
   return r;
 }
 template <int D, int NB>
 size_t space_of(const RowsPlan& r, void* base, RowsSpace* ws) {
-  if (!r.cut) return 0;
+  if (r.pieces == 1) return 0;
   constexpr int R = 8 * NB;
   const size_t o = static_cast<size_t>(r.blocks) * 2 * R * D * 4, ml = static_cast<size_t>(r.blocks) * 2 * R * 8;
   if (ws) {
@@ -837,10 +891,13 @@ omq_status launch_rows(const AttnParams& p, int max_rows, void* space, cudaStrea
   RowsSpace ws = {};
   space_of<D, NB>(r, space, &ws);
   launch_k(kv_rows_kernel<D, NB>, dim3(static_cast<unsigned>(r.blocks)), 32 * W, F::SMEM, st, p,
-           static_cast<int>(r.tiles), max_rows, r.cut ? 1 : 0, ws);
+           static_cast<int>(r.tiles), max_rows, r.pieces, ws);
   const omq_status s = launch_status();
-  if (s != OMQ_OK || !r.cut) return s;
-  launch_k(kv_rows_join_kernel<D, NB>, dim3(static_cast<unsigned>(r.blocks), 8 * NB), 128, 0, st, p, max_rows, ws);
+  if (s != OMQ_OK || r.pieces == 1) return s;
+  const int64_t most = static_cast<int64_t>(p.max_q) * p.G;
+  launch_k(kv_rows_join_kernel<D, NB>,
+           dim3(static_cast<unsigned>(r.blocks), static_cast<unsigned>(most < F::R ? most : F::R)),
+           128, 0, st, p, ws);
   return launch_status();
 }
 
