@@ -309,36 +309,44 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
   const int w0 = run0 + warp;
   const int32_t* row_table = p.table + static_cast<int64_t>(b) * p.width;
   const int n_cell = (vis_max + kCell - 1) / kCell;
-  // Copies run `run` into stage s; returns which of its four cells exist (bit i: cell i).
-  auto fetch = [&](int run, int s) -> uint32_t {
-    const int ci = run * NCELL + lane;
+  // The warp's runs are w0, w0 + W, ..; lane 4 n + i holds the source of cell i of the n-th of
+  // eight of them (NULL: not there), looked up once for the eight.
+  const uint8_t* src = nullptr;
+  uint32_t there8 = 0;                   // the cells that are there, four bits a run
+  auto look = [&](int run) {
+    const int ci = (run + (lane >> 2) * W) * NCELL + (lane & 3);
     int id = -1;
     uint32_t pg = 0;
-    if (lane < NCELL && ci < n_cell) {
+    if (ci < n_cell) {
       pg = p.pool.shift >= 0 ? static_cast<uint32_t>(ci) >> p.pool.shift
                              : static_cast<uint32_t>(ci) / static_cast<uint32_t>(p.pool.cells);
       id = row_table[pg];
     }
-    const bool have = id >= 0 && id < p.pool.n_pages;
-    const uint32_t mask = __ballot_sync(0xffffffffu, have);
-    if (lane == 0) bar_expect(bars + 8 * s, __popc(mask) * C::BYTES);
+    src = id < 0 || id >= p.pool.n_pages
+              ? nullptr
+              : p.pool.data + ((static_cast<int64_t>(id) * p.pool.Hkv + kvh) * p.pool.cells +
+                               (ci - static_cast<int>(pg) * p.pool.cells)) *
+                                  static_cast<int64_t>(C::BYTES);
+    there8 = __ballot_sync(0xffffffffu, src != nullptr);
+  };
+  // Copies the n-th run (of w0, w0 + W, ..) into stage s; returns which of its cells there are.
+  auto fetch = [&](int n, uint32_t s) -> uint32_t {
+    if ((n & 7) == 0) look(w0 + n * W);
+    const uint32_t cells = (there8 >> (4 * (n & 7))) & 15u;
+    if (lane == 0) bar_expect(bars + 8 * s, __popc(cells) * C::BYTES);
     __syncwarp();
-    if (have) {
-      const uint8_t* src = p.pool.data + ((static_cast<int64_t>(id) * p.pool.Hkv + kvh) * p.pool.cells +
-                                          (ci - static_cast<int>(pg) * p.pool.cells)) *
-                                             static_cast<int64_t>(C::BYTES);
-      bulk_load(ring + s * F::STAGE + lane * F::PITCH, src, C::BYTES, bars + 8 * s);
-    }
-    return mask;
+    if ((lane >> 2) == (n & 7) && src)
+      bulk_load(ring + s * F::STAGE + (lane & 3) * F::PITCH, src, C::BYTES, bars + 8 * s);
+    return cells;
   };
 
   uint32_t have = 0;                     // four bits a stage: its cells that are there
   int fetched = 0;
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k)
-    if (w0 + k * W < n_run) {
-      const uint32_t st = (it + k) % STAGES;
-      have |= fetch(w0 + k * W, st) << (4 * st);
+  for (int n = 0; n < STAGES - 1; ++n)
+    if (w0 + n * W < n_run) {
+      const uint32_t st = (it + n) % STAGES;
+      have |= fetch(n, st) << (4 * st);
       ++fetched;
     }
 
@@ -427,16 +435,12 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
       const int ahead = run + (STAGES - 1) * W;
       if (ahead < n_run) {
         const uint32_t st = (it + STAGES - 1) % STAGES;
-        have = (have & ~(15u << (4 * st))) | (fetch(ahead, st) << (4 * st));
+        have = (have & ~(15u << (4 * st))) | (fetch(fetched, st) << (4 * st));
         ++fetched;
       }
-      int got = 0;
-      if (lane == 0)
-        got = bar_wait(bars + 8 * s, (it / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
-                       DEV_ERR_TMA_WAIT);
-      got = __shfl_sync(0xffffffffu, got, 0);
       // every lane observes the completed phase itself before it reads what the copies wrote
-      if (!got || !bar_try(bars + 8 * s, (it / STAGES) & 1)) got = 0;
+      const bool got = bar_wait(bars + 8 * s, (it / STAGES) & 1, &g_rows_error, &g_rows_limit_ns,
+                                DEV_ERR_TMA_WAIT);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
