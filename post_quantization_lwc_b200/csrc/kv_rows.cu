@@ -839,21 +839,17 @@ RowsPlan plan_rows(const AttnParams& p, int max_rows) {
   const int64_t items = r.tiles * p.pool.Hkv * p.n_req;
   const int64_t runs = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, STEP);
   const int64_t room = (NB == 1 ? 3 : 2) * static_cast<int64_t>(num_sms());
-  // whole items where a block's four warps have at most two runs each, or where the blocks fill
-  // the SMs many times over (a long item is then a small part of the whole)
-  if (runs <= 2 * W || items >= 8 * room) {
-    r.pieces = 1;
-    r.blocks = items;
-    return r;
-  }
-  // Equal shares of each item while all blocks are resident at once, if the requests are as long
-  // as each other (there is one) or the shares short; no block then handles two items, which
-  // costs it a second round of latencies (one request of 2049 tokens, 32 heads: 10.9 us against
-  // 15.7). Else the even line.
-  int64_t pieces = room / items;
+  // Equal shares of each item while all blocks are resident at once, two up to 2.5 times that,
+  // then whole items, if the requests are as long as each other (there is one), a share is at
+  // most 16 runs a warp, or the blocks are so many that a long item is a small part of the
+  // whole. No block then handles two items, which costs it a second round of latencies: one
+  // request of 2049 tokens and 32 heads takes 10.8 us against 15.7 on the even line, 33 of up to
+  // 4001 tokens 23.3 against 28.3, 64 of up to 8192 82.7 against 87.4. The even line else: it
+  // does not depend on how the lengths, which the host does not know, are spread.
+  int64_t pieces = items <= room ? room / items : 2 * items <= 5 * room ? 2 : 1;
   const int64_t useful = ceil_div(runs, W);
   if (pieces > useful) pieces = useful;
-  if (pieces > 1 && (p.n_req == 1 || ceil_div(runs, pieces) <= 4 * W)) {
+  if (p.n_req == 1 || ceil_div(runs, pieces) <= 16 * W || items >= 8 * room) {
     r.pieces = static_cast<int>(pieces);
     r.blocks = items * pieces;
     return r;

@@ -151,6 +151,24 @@ def test_long_contexts(omq, cuda_device, lens, new, Hkv, G, D, page, dt):
     s.check(out, lse, rows=97)
 
 
+@pytest.mark.parametrize("n_req,Hkv,G,new,wide", [(40, 8, 1, 1, 9600), (150, 3, 6, 2, 12000),
+                                                  (300, 2, 1, 1, 9000)])
+def test_ragged_requests_under_a_wide_table(omq, cuda_device, n_req, Hkv, G, new, wide):
+    """Lengths far below what the table allows, one far above the others: the blocks share one
+    line of all requests' runs (300 requests: found over several chunks of the block)."""
+    rng = np.random.default_rng(n_req)
+    lens = rng.integers(new, 90, n_req)
+    lens[3], lens[n_req - 2] = 3000, 0
+    cnt = np.minimum(np.full(n_req, new), lens)
+    s = Setup(cuda_device, lens, cnt, Hkv, G, 64, 16, "f16", seed=5)
+    table = torch.full((n_req, wide // 16), -1, dtype=torch.int32, device=cuda_device)
+    table[:, :s.table.shape[1]] = s.args[2]
+    s.args[2] = table
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse)
+
+
 @pytest.mark.parametrize("new", [1, 6, 150])
 def test_other_types_scales_and_sizes(omq, cuda_device, new):
     """Output of another type, a given scale, queries of very different size, values far from
