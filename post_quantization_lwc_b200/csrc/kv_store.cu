@@ -19,23 +19,6 @@ namespace omq {
 namespace kv {
 namespace {
 
-// 4 consecutive elements starting at a multiple of 4.
-__device__ __forceinline__ void load4(const void* p, int64_t i, omq_dtype dt, float* v) {
-  if (dt == OMQ_F32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  } else {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
-    if (dt == OMQ_F16) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a.x));
-      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&a.y));
-      v[0] = x.x; v[1] = x.y; v[2] = y.x; v[3] = y.y;
-    } else {
-      v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
-    }
-  }
-}
 __device__ __forceinline__ void store4(void* p, int64_t i, omq_dtype dt, const float* v) {
   if (dt == OMQ_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
@@ -64,7 +47,94 @@ __device__ __forceinline__ uint8_t* slot_cell(const Pool& p, int slot, int head,
                       static_cast<int64_t>(cell_bytes);
 }
 
-template <int D>
+// E consecutive elements starting at a multiple of E (4 or 8).
+template <int E, omq_dtype DT>
+__device__ __forceinline__ void load_run(const void* p, int64_t i, float2 (&v)[E / 2]) {
+  if constexpr (DT == OMQ_F32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+      const float4 a = __ldg(q + k);
+      v[2 * k] = make_float2(a.x, a.y);
+      v[2 * k + 1] = make_float2(a.z, a.w);
+    }
+  } else {
+    uint32_t w[E / 2];
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if constexpr (E == 8) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    } else {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(q));
+      w[0] = a.x; w[1] = a.y;
+    }
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      if (DT == OMQ_F16) v[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      else v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    }
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_run(void* p, int64_t i, omq_dtype dt, const float2 (&v)[E / 2]) {
+  if (dt == OMQ_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) q[k] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+    return;
+  }
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    if (dt == OMQ_F16) {
+      const __half2 x = __floats2half2_rn(v[k].x, v[k].y);
+      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(v[k].x, v[k].y);
+      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  uint16_t* q = static_cast<uint16_t*>(p) + i;
+  if constexpr (E == 8) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// round(v / h) of E values, each with v / h the correctly rounded quotient, as 1.5 2^23 plus the
+// integer (its low mantissa bits hold it): the product with the reciprocal where that provably
+// rounds alike, and one vote of the lanes that are here for the others. The product is off by at
+// most 2^-23 |v / h| (two roundings), so at most thr = 0.49999 - 2^-22 max |v / h| from its
+// integer it rounds as the quotient does (with the fixed 0.499 of round_quotient 40% of the
+// warps had a lane that took the division). thr < 0: |v / h| may be 2000 or more. (Where the compiler contracts
+// the product with the sums after it, the product is closer to v / h still.)
+template <int E>
+__device__ __forceinline__ void round_run(const float2 (&v)[E / 2], float h, float hinv, float thr,
+                                          float2 (&t)[E / 2]) {
+  const float2 magic = both(12582912.f), hi = both(hinv);
+  float far = 0.f;
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) {
+    const float2 u = __fmul2_rn(v[k], hi);
+    t[k] = __fadd2_rn(u, magic);
+    const float2 d = __fadd2_rn(u, neg2(__fadd2_rn(t[k], neg2(magic))));
+    far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+  }
+  const bool slow = !(far <= thr);
+  if (__any_sync(__activemask(), slow)) {
+    if (slow) {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        // (integers beyond 2^22 end in a clamped code, whichever they are)
+        const float x = fminf(fmaxf(round_quotient(v[k].x, h, hinv), -4194303.f), 4194303.f);
+        const float y = fminf(fmaxf(round_quotient(v[k].y, h, hinv), -4194303.f), 4194303.f);
+        t[k] = make_float2(__fadd_rn(x, 12582912.f), __fadd_rn(y, 12582912.f));
+      }
+    }
+  }
+}
+
+template <int D, omq_dtype DT>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
   pdl_wait();
   pdl_launch();
@@ -78,36 +148,33 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
                      (lane >> 3);
   if (id - (lane >> 3) >= total) return;              // warp-uniform
   const bool in = id < total;
-  const int64_t t = in ? id / rows : 0;
-  const int r = in ? static_cast<int>(id - t * rows) : 0;
+  const uint32_t t = in ? static_cast<uint32_t>(id) / static_cast<uint32_t>(rows) : 0u;
+  const int r = in ? static_cast<int>(id - static_cast<int64_t>(t) * rows) : 0;
   const int which = r < nq ? 0 : r < nq + p.pool.Hkv ? 1 : 2;
   const int head = which == 0 ? r : which == 1 ? r - nq : r - nq - p.pool.Hkv;
   const void* src = which == 0 ? p.q : which == 1 ? p.k : p.v;
   const int64_t ld = which == 0 ? p.q_ld : which == 1 ? p.k_ld : p.v_ld;
-  const int64_t base = t * ld + static_cast<int64_t>(head) * D;
-  float a[E], b[E];                       // elements E sub + e and D/2 + E sub + e
-#pragma unroll
-  for (int e = 0; e < E; e += 4) {
-    load4(src, base + E * sub + e, p.dt, a + e);
-    load4(src, base + D / 2 + E * sub + e, p.dt, b + e);
-  }
+  const int64_t base = t * ld + static_cast<int64_t>(head) * D + E * sub;
+  float2 a[E / 2], b[E / 2];              // elements E sub + e and D/2 + E sub + e
+  load_run<E, DT>(src, base, a);
+  load_run<E, DT>(src, base + D / 2, b);
   const int slot = __ldg(p.slots + t);
   const int pos = p.positions ? __ldg(p.positions + t) : 0;
-  const bool live = in && slot >= 0 && slot < p.pool.n_pages * p.pool.page && pos >= 0 && (!p.rope || pos < p.n_pos);
+  const bool live = in && slot >= 0 && slot < p.pool.n_pages * p.pool.page && pos >= 0 &&
+                    (!p.rope || pos < p.n_pos);
   if (which < 2 && p.rope && live) {
-    const float* cp = p.rope + static_cast<int64_t>(pos) * (D / 2) + E * sub;
-    const float* sp = cp + p.n_pos * (D / 2);
+    const int64_t at = static_cast<int64_t>(pos) * (D / 2) + E * sub;
+    float2 c[E / 2], s[E / 2];
+    load_run<E, OMQ_F32>(p.rope, at, c);
+    load_run<E, OMQ_F32>(p.rope, at + p.n_pos * (D / 2), s);
 #pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      float c[4], s[4];
-      load4(cp, e, OMQ_F32, c);
-      load4(sp, e, OMQ_F32, s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = a[e + i], y = b[e + i];
-        a[e + i] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
-        b[e + i] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
-      }
+    for (int k = 0; k < E / 2; ++k) {
+      // (scalar: the paired product and sum would be contracted to one rounding)
+      const float2 x = a[k], y = b[k];
+      a[k].x = __fsub_rn(__fmul_rn(x.x, c[k].x), __fmul_rn(y.x, s[k].x));
+      a[k].y = __fsub_rn(__fmul_rn(x.y, c[k].y), __fmul_rn(y.y, s[k].y));
+      b[k].x = __fadd_rn(__fmul_rn(y.x, c[k].x), __fmul_rn(x.x, s[k].x));
+      b[k].y = __fadd_rn(__fmul_rn(y.y, c[k].y), __fmul_rn(x.y, s[k].y));
     }
   }
   // the learned scales are per kv head: q head j has those of kv head j / G
@@ -115,43 +182,48 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
   const float* sc = which == 2 ? p.s_o : p.s_a;
   if (sc) {
     const int64_t o = static_cast<int64_t>(hk) * D + E * sub;
+    float2 u[E / 2], w[E / 2];
+    if (which == 2 && p.delta_o) {
+      load_run<E, OMQ_F32>(p.delta_o, o, u);
+      load_run<E, OMQ_F32>(p.delta_o, o + D / 2, w);
 #pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      float u[4], w[4];
-      load4(sc, o + e, OMQ_F32, u);
-      load4(sc, o + D / 2 + e, OMQ_F32, w);
-      if (which == 2 && p.delta_o) {
-        float du[4], dw[4];
-        load4(p.delta_o, o + e, OMQ_F32, du);
-        load4(p.delta_o, o + D / 2 + e, OMQ_F32, dw);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[e + i] = __fsub_rn(a[e + i], du[i]);
-          b[e + i] = __fsub_rn(b[e + i], dw[i]);
-        }
+      for (int k = 0; k < E / 2; ++k) {
+        a[k] = __fadd2_rn(a[k], neg2(u[k]));
+        b[k] = __fadd2_rn(b[k], neg2(w[k]));
       }
+    }
+    load_run<E, OMQ_F32>(sc, o, u);
+    load_run<E, OMQ_F32>(sc, o + D / 2, w);
+    if (which == 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[e + i] = which == 1 ? __fmul_rn(a[e + i], u[i]) : __fdiv_rn(a[e + i], u[i]);
-        b[e + i] = which == 1 ? __fmul_rn(b[e + i], w[i]) : __fdiv_rn(b[e + i], w[i]);
+      for (int k = 0; k < E / 2; ++k) {
+        a[k] = __fmul2_rn(a[k], u[k]);
+        b[k] = __fmul2_rn(b[k], w[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        a[k] = make_float2(__fdiv_rn(a[k].x, u[k].x), __fdiv_rn(a[k].y, u[k].y));
+        b[k] = make_float2(__fdiv_rn(b[k].x, w[k].x), __fdiv_rn(b[k].y, w[k].y));
       }
     }
   }
   const bool quant = which != 0 || p.quant_q;
   float vmax = -INFINITY, vmin = INFINITY;
-  bool bad = false;                       // a NaN or an infinity in the row
+  float fin = 0.f;                        // NaN if the row holds a NaN or an infinity
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    vmax = fmaxf(vmax, fmaxf(a[e], b[e]));
-    vmin = fminf(vmin, fminf(a[e], b[e]));
-    bad |= !(fabsf(a[e]) < INFINITY) || !(fabsf(b[e]) < INFINITY);
+  for (int k = 0; k < E / 2; ++k) {
+    vmax = fmaxf(vmax, fmaxf(fmaxf(a[k].x, a[k].y), fmaxf(b[k].x, b[k].y)));
+    vmin = fminf(vmin, fminf(fminf(a[k].x, a[k].y), fminf(b[k].x, b[k].y)));
+    const float2 z = __ffma2_rn(a[k], both(0.f), __fmul2_rn(b[k], both(0.f)));
+    fin += z.x + z.y;
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) {
     vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
     vmin = fminf(vmin, __shfl_xor_sync(0xffffffffu, vmin, o));
   }
-  bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 24)) & 0xffu;
+  const bool bad = (__ballot_sync(0xffffffffu, fin != fin) >> (lane & 24)) & 0xffu;
   if (!live) return;
   if (quant) {
     const float Q = which == 0 ? p.Qa : 15.f;
@@ -162,24 +234,58 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
       g.z = 0.f;
     }
     const float hinv = __frcp_rn(g.h);
-    const float z = static_cast<float>(z_to_i32(g.z));
+    const int zi = z_to_i32(g.z);
+    const float umax = fmaxf(fabsf(vmax), fabsf(vmin)) * hinv;
+    const float thr = umax < 2000.f ? 0.49999f - 2.384185791015625e-07f * umax : -1.f;
+    float2 ta[E / 2], tb[E / 2];
+    round_run<E>(a, g.h, hinv, thr, ta);
+    round_run<E>(b, g.h, hinv, thr, tb);
+    // code = clamp(round + z): where |z| is small enough for the exact integers, in integers;
+    // else (a row hundreds of times further from zero than it spreads) in binary32 as defined
+    const int off = zi - 0x4B400000, top = static_cast<int>(Q);
     uint32_t wa = 0, wb = 0;
+    if (which == 0 && fabsf(g.z) < 4000000.f) {
+      // c - z = clamp(round, -z, Q - z), all exact integers
+      const float lo = -g.z, hi = Q - g.z;
+      auto value = [&](float2 t) {
+        const float2 r = __fadd2_rn(t, both(-12582912.f));
+        return __fmul2_rn(make_float2(fminf(fmaxf(r.x, lo), hi), fminf(fmaxf(r.y, lo), hi)), both(g.h));
+      };
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float ca = fminf(fmaxf(__fadd_rn(round_quotient(a[e], g.h, hinv), g.z), 0.f), Q);
-      const float cb = fminf(fmaxf(__fadd_rn(round_quotient(b[e], g.h, hinv), g.z), 0.f), Q);
-      if (which == 0) {
-        a[e] = __fmul_rn(__fsub_rn(ca, z), g.h);
-        b[e] = __fmul_rn(__fsub_rn(cb, z), g.h);
-      } else {
-        wa |= small_uint(ca) << (4 * e);
-        wb |= small_uint(cb) << (4 * e);
+      for (int k = 0; k < E / 2; ++k) {
+        a[k] = value(ta[k]);
+        b[k] = value(tb[k]);
+      }
+    } else if (fabsf(g.z) < 4000000.f) {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        const int a0 = min(max(__float_as_int(ta[k].x) + off, 0), top);
+        const int a1 = min(max(__float_as_int(ta[k].y) + off, 0), top);
+        const int b0 = min(max(__float_as_int(tb[k].x) + off, 0), top);
+        const int b1 = min(max(__float_as_int(tb[k].y) + off, 0), top);
+        wa |= static_cast<uint32_t>(a0 | a1 << 4) << (8 * k);
+        wb |= static_cast<uint32_t>(b0 | b1 << 4) << (8 * k);
+      }
+    } else {
+      const float z = static_cast<float>(zi);
+      auto code = [&](float x) {
+        return fminf(fmaxf(__fadd_rn(round_quotient(x, g.h, hinv), g.z), 0.f), Q);
+      };
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        const float a0 = code(a[k].x), a1 = code(a[k].y), b0 = code(b[k].x), b1 = code(b[k].y);
+        if (which == 0) {
+          a[k] = make_float2(__fmul_rn(__fsub_rn(a0, z), g.h), __fmul_rn(__fsub_rn(a1, z), g.h));
+          b[k] = make_float2(__fmul_rn(__fsub_rn(b0, z), g.h), __fmul_rn(__fsub_rn(b1, z), g.h));
+        } else {
+          wa |= (small_uint(a0) | small_uint(a1) << 4) << (8 * k);
+          wb |= (small_uint(b0) | small_uint(b1) << 4) << (8 * k);
+        }
       }
     }
     if (which != 0) {
       int row = 0;
       uint8_t* cell = slot_cell(p.pool, slot, head, C::BYTES, &row);
-      if (!cell) return;
       uint8_t* codes = cell + (which == 1 ? C::K : C::V) + row * C::ROW + sub * (E / 2);
       if (E == 8) {
         *reinterpret_cast<uint32_t*>(codes) = wa;
@@ -190,17 +296,14 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
       }
       if (sub == 0) {
         *reinterpret_cast<float*>(cell + (which == 1 ? C::KH : C::VH) + 4 * row) = g.h;
-        *reinterpret_cast<int32_t*>(cell + (which == 1 ? C::KZ : C::VZ) + 4 * row) = z_to_i32(g.z);
+        *reinterpret_cast<int32_t*>(cell + (which == 1 ? C::KZ : C::VZ) + 4 * row) = zi;
       }
       return;
     }
   }
-  const int64_t o = (t * p.Hq + head) * D + E * sub;
-#pragma unroll
-  for (int e = 0; e < E; e += 4) {
-    store4(p.q_out, o + e, p.q_dt, a + e);
-    store4(p.q_out, o + D / 2 + e, p.q_dt, b + e);
-  }
+  const int64_t o = (static_cast<int64_t>(t) * p.Hq + head) * D + E * sub;
+  store_run<E>(p.q_out, o, p.q_dt, a);
+  store_run<E>(p.q_out, o + D / 2, p.q_dt, b);
 }
 
 // Read-back: four values a lane, so a warp's stores are whole rows. v = (c - z) h, c - z exact
@@ -238,6 +341,13 @@ __global__ void __launch_bounds__(256) kv_read_kernel(ReadParams p) {
   store4(p.v, row_id * D + 4 * l, p.dt, v);
 }
 
+template <int D>
+void launch_append_d(const AppendParams& p, unsigned grid, int threads, cudaStream_t st) {
+  if (p.dt == OMQ_F32) launch_k(kv_append_kernel<D, OMQ_F32>, grid, threads, 0, st, p);
+  else if (p.dt == OMQ_F16) launch_k(kv_append_kernel<D, OMQ_F16>, grid, threads, 0, st, p);
+  else launch_k(kv_append_kernel<D, OMQ_BF16>, grid, threads, 0, st, p);
+}
+
 }  // namespace
 
 omq_status launch_append(const AppendParams& p, int64_t D, cudaStream_t st) {
@@ -245,8 +355,8 @@ omq_status launch_append(const AppendParams& p, int64_t D, cudaStream_t st) {
   // small calls spread over the SMs in blocks of one warp
   const int threads = ceil_div(rows, 4) <= 4 * num_sms() ? 32 : 256;
   const unsigned grid = static_cast<unsigned>(ceil_div(rows, 4 * (threads / 32)));
-  if (D == 128) launch_k(kv_append_kernel<128>, grid, threads, 0, st, p);
-  else launch_k(kv_append_kernel<64>, grid, threads, 0, st, p);
+  if (D == 128) launch_append_d<128>(p, grid, threads, st);
+  else launch_append_d<64>(p, grid, threads, st);
   return launch_status();
 }
 
