@@ -641,7 +641,7 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * dense, F16 or BF16; lse [T, Hq] float32 (natural log of the softmax's denominator) or NULL.
  * The codes are exact operands and sums, statistics and steps are float32; the weights are
  * rounded to float16 relative to the row's largest, q exactly unless an element is 2^-28 of
- * the largest of the rows it is processed with. For a request of more than 32 query rows per kv
+ * the largest of the rows it is processed with. For a request of more than 64 query rows per kv
  * head (rows = tokens x Hq / Hkv), k and v themselves are float16 operands, rounded once (so
  * |k scale log2 e| and |v| below 65504). Results are bitwise reproducible on one device.
  * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL).

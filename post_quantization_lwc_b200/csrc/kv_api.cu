@@ -61,17 +61,29 @@ omq_status check_attn(const omq_kv_attn_args* a) {
   return OMQ_OK;
 }
 
-// Query rows per kv head up to which a request goes to the row kernel.
-constexpr int kFew = 32;
+// Query rows per kv head up to which a request goes to the row kernel, whose time grows with the
+// rows (it expands the codes again for every 16), while the tile kernel's does not up to 512.
+// Row / tile kernel, us, at 64 rows and at 128: 8 requests of 4096 tokens and 8 kv heads 48 / 70
+// and 118 / 71; 32 of 2048 107 / 149 and 195 / 154; one of 65536 84 / 126 and 166 / 127; one of
+// 4096 tokens and 32 kv heads 33 / 44 and 48 / 45; 8 kv heads of 64 values 15 / 19 and 18 / 20.
+constexpr int kFew = 64;
 
 int64_t most_rows(const omq_kv_attn_args* a) { return a->max_q * (a->Hq / a->pool.Hkv); }
 bool uses_rows(const omq_kv_attn_args* a) { return most_rows(a) <= kFew || a->n_req > 1; }
-
+bool uses_tiles(const omq_kv_attn_args* a) { return most_rows(a) > kFew; }
+// Where both kernels run, each takes the requests of its kind, by the lengths on the device.
+int tiles_min(const omq_kv_attn_args* a) { return uses_rows(a) ? kFew + 1 : 0; }
 kv::AttnParams attn_params(const omq_kv_attn_args* a) {
   return kv::AttnParams{view(a->pool), static_cast<int>(a->n_req), a->T, static_cast<int>(a->Hq),
                         static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
                         static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
                         a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
+}
+// The kernels run one after the other and share the workspace.
+size_t attn_space(const omq_kv_attn_args* a, const kv::AttnParams& p) {
+  const size_t r = uses_rows(a) ? kv::attn_rows_space(p, a->pool.D, kFew) : 0;
+  const size_t t = uses_tiles(a) ? kv::attn_tiles_space(p, a->pool.D, tiles_min(a)) : 0;
+  return r > t ? r : t;
 }
 
 }  // namespace
@@ -169,7 +181,7 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
 size_t omq_kv_attn_workspace_bytes(const omq_kv_attn_args* a) {
   if (check_attn(a) != OMQ_OK) return 0;
   const kv::AttnParams p = attn_params(a);
-  return uses_rows(a) ? kv::attn_rows_space(p, a->pool.D, kFew) : 0;
+  return attn_space(a, p);
 }
 
 omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_bytes,
@@ -177,15 +189,10 @@ omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_byt
   KV_TRY(check_attn(a));
   const kv::AttnParams p = attn_params(a);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (uses_rows(a)) {
-    const size_t need = kv::attn_rows_space(p, a->pool.D, kFew);
-    if (need && (!workspace || ws_bytes < need)) return OMQ_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return OMQ_ERR_ALIGN;
-  }
-  // both kernels where the requests differ: each takes those of its kind, by the lengths on
-  // the device
-  if (most_rows(a) > kFew)
-    KV_TRY(kv::launch_attn_tiles(p, a->pool.D, a->n_req == 1 ? 0 : kFew + 1, st));
+  const size_t need = attn_space(a, p);
+  if (need && (!workspace || ws_bytes < need)) return OMQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return OMQ_ERR_ALIGN;
+  if (uses_tiles(a)) KV_TRY(kv::launch_attn_tiles(p, a->pool.D, tiles_min(a), workspace, st));
   return uses_rows(a) ? kv::launch_attn_rows(p, a->pool.D, kFew, workspace, st) : OMQ_OK;
 }
 

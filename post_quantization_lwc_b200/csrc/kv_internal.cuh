@@ -113,7 +113,9 @@ omq_status launch_attn_rows(const AttnParams& p, int64_t D, int max_rows, void* 
                             cudaStream_t st);
 size_t attn_rows_space(const AttnParams& p, int64_t D, int max_rows);   // bytes of `space`
 // Attention of the requests with at least min_rows query rows per kv head, 512 rows a CTA pair.
-omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, cudaStream_t st);
+omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, void* space,
+                             cudaStream_t st);
+size_t attn_tiles_space(const AttnParams& p, int64_t D, int min_rows);
 
 // Per translation unit with barrier waits: read and clear its error flag, set its wait limit
 // (the counterparts of take_device_error and set_wait_limit).

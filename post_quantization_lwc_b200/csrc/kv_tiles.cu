@@ -18,6 +18,11 @@
 // to the pair's operands: K of 64 keys, V's 64 columns of all 128 keys (for D = 64 the second
 // CTA's V half stays zero). The order in which a word yields its 8 values (0 4 1 5 2 6 3 7) is
 // kept in both operands (Q is staged in the same order) and undone where o is written.
+// Where the items are few for the 74 pairs, a pair takes an equal share of an item's keys and
+// leaves o and (m, l) in float32; a second kernel joins the parts in their order (one request
+// under 65536 tokens, 8 x 4 heads: 64 new tokens 950 -> 130 us, 512 new ones 1019 -> 527).
+// Which item a pair has follows from the lengths on the device, so that requests of another
+// kind (a step with one chunk and many single tokens) take no pairs.
 // Warp roles (512 threads; registers are shared out again at the start, 200 a softmax thread
 // and 56 the others):
 //   0-3, 4-7  softmax of subtile 0 / 1, a row a thread; they also stage Q and write o
@@ -53,6 +58,7 @@ constexpr int NR = 3;                 // raw stages
 constexpr int THREADS = 512;
 constexpr int REGS = 128, REGS_SOFTMAX = 200, REGS_OTHER = 56;   // per thread: launch, after
 static_assert(2 * REGS >= REGS_SOFTMAX + REGS_OTHER, "the shares come out of the launch's registers");
+constexpr int ROWS = 512;             // query rows of a pair
 constexpr float GROW = 8.f;           // growth of a row's maximum (log2) that moves m_i
 
 template <int D>
@@ -272,9 +278,78 @@ __device__ __forceinline__ void expand4(const uint4& w, const RowSteps& r, uint3
   }
 }
 
-template <int D>
+// Partial results of pairs that share an item's keys: o (not divided) of part i at
+// o[(i D / 4 + column / 4) 512 + row], columns in the operands' order; (reference, sum) at
+// ml[512 i + row], the sum 0 where there was no key (o is then not written). desc: the item's
+// request and tile, request -1: none.
+struct TilesSpace {
+  float4* o;
+  float2* ml;
+  int2* desc;
+};
+
+// Row tiles that request b has for this kernel.
+__device__ __forceinline__ int req_tiles(const AttnParams& p, int b, int min_rows) {
+  const int first = p.cu[b];
+  const int n = min(max(p.cu[b + 1] - first, 0), p.max_q);
+  if (first < 0 || first >= p.T || n * p.G < min_rows) return 0;
+  return (static_cast<int>(min(static_cast<int64_t>(n), p.T - first)) * p.G + ROWS - 1) / ROWS;
+}
+// The at-th row tile of all requests, in their order, a request's last (it sees the most keys)
+// first: (request, tile), request -1 behind the last. For the whole block.
+__device__ __forceinline__ int2 find_tile(const AttnParams& p, int at, int min_rows) {
+  if (p.n_req == 1) {
+    const int n = req_tiles(p, 0, min_rows);
+    return at < n ? make_int2(0, n - 1 - at) : make_int2(-1, 0);
+  }
+  __shared__ int sums[THREADS / 32];
+  __shared__ int2 found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) found = make_int2(-1, 0);
+  for (int c = 0; c < p.n_req; c += THREADS) {
+    const int b = c + threadIdx.x;
+    const int n = b < p.n_req ? req_tiles(p, b, min_rows) : 0;
+    int end = n;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += o;
+    }
+    if (lane == 31) sums[warp] = end;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w == warp) end += all;
+      all += sums[w];
+    }
+    if (at < end && at >= end - n) found = make_int2(b, end - 1 - at);
+    __syncthreads();
+    if (at < all) break;
+    at -= all;
+  }
+  return found;
+}
+
+// Eight results in the operands' order (elements 0 .. 7 stand at 0 2 4 6 1 3 5 7), 16 bits each.
+__device__ __forceinline__ uint4 out_eight(const float* v, int dt) {
+  uint32_t w[4];
+  const int e0[4] = {0, 4, 1, 5}, e1[4] = {2, 6, 3, 7};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (dt == OMQ_F16) {
+      w[k] = pack_h2(v[e0[k]], v[e1[k]]);
+    } else {
+      const __nv_bfloat162 q = __floats2bfloat162_rn(v[e0[k]], v[e1[k]]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int D, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    kv_tiles_kernel(AttnParams p, int tiles, int min_rows) {
+    kv_tiles_kernel(AttnParams p, int pieces, int min_rows, TilesSpace ws) {
   using F = TilesCfg<D>;
   using C = CellT<D>;
   constexpr float kLog2e = 1.4426950408889634f;
@@ -289,21 +364,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + F::MISS);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + F::SLOT);
 
-  // the last tiles of the requests see the most keys: they go first
-  const int item = blockIdx.x >> 1;
-  const int per = p.n_req * p.pool.Hkv;
-  const int tile = tiles - 1 - item / per;
-  const int kvh = (item % per) % p.pool.Hkv;
-  const int b = (item % per) / p.pool.Hkv;
+  // part of the launch: a share of an item's keys
+  const int part = blockIdx.x >> 1;
+  const int item = SPLIT ? part / pieces : part;
+  const int kvh = item % p.pool.Hkv;
 
   pdl_wait();
   pdl_launch();
+  const int2 at = find_tile(p, item / p.pool.Hkv, min_rows);
+  const int b = at.x, tile = at.y;
+  if (SPLIT && rank == 0 && threadIdx.x == 0 && part == item * pieces) ws.desc[item] = at;
+  if (b < 0) return;                                           // the same for both CTAs
   const int len = min(max(p.lens[b], 0), p.width * p.pool.page);
   const int first = p.cu[b];
   const int n_new = min(max(p.cu[b + 1] - first, 0), p.max_q);
   const int rows = n_new * p.G;
-  const int row0 = tile * 512;
-  if (row0 >= rows || rows < min_rows || first < 0) return;    // the same for both CTAs
+  const int row0 = tile * ROWS;
 
   auto row_vis = [&](int r) {
     if (r >= rows || first + r / p.G >= p.T) return 0;
@@ -311,8 +387,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   };
   const int vis_max = row_vis(min(row0 + 511, rows - 1));
   // tiles of keys that the subtiles see
-  const int nt0 = (row_vis(min(row0 + 255, rows - 1)) + KT - 1) / KT;
-  const int nt1 = row0 + 256 < rows ? (vis_max + KT - 1) / KT : 0;
+  int nt0 = (row_vis(min(row0 + 255, rows - 1)) + KT - 1) / KT;
+  int nt1 = row0 + 256 < rows ? (vis_max + KT - 1) / KT : 0;
+  int key0 = 0;                                                // the part's first key
+  if (SPLIT) {
+    const int share = (max(nt0, nt1) + pieces - 1) / pieces, t0 = (part - item * pieces) * share;
+    nt0 = min(max(nt0 - t0, 0), share);
+    nt1 = min(max(nt1 - t0, 0), share);
+    key0 = t0 * KT;
+  }
   const int nt = max(nt0, nt1);
   const int n_cell = (vis_max + kCell - 1) / kCell;
 
@@ -432,8 +515,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // the roles' code missed the instruction cache in 30% of its requests, and 8192 tokens of
       // 8 x 4 heads took 827 us instead of 592).
       const uint32_t gone = miss[j & 7];
-      if (any_post || j * KT + KT > vis_warp || gone != 0) {
-        const int lim = vis - j * KT;
+      if (any_post || key0 + j * KT + KT > vis_warp || gone != 0) {
+        const int lim = vis - key0 - j * KT;
 #pragma unroll 1
         for (int c = 0; c < KT; c += 16) {
           float x[16];
@@ -524,7 +607,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ---- o
     if (ok && my_nt > 0)
       ok = wait_for(sb + F::OF + 8 * s, (my_nt - 1) & 1, abort_flag, DEV_ERR_EPI_WAIT);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (SPLIT) {
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_after();
+        const int64_t at_row = row - row0;
+        if (have_row) ws.ml[static_cast<int64_t>(part) * ROWS + at_row] = make_float2(m, l);
+        float4* dst = ws.o + static_cast<int64_t>(part) * (D / 4) * ROWS + at_row;
+        if (my_nt > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tm_ld16(tO + c, o);
+            tm_ld_wait();
+            if (have_row && l != 0.f) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                dst[static_cast<int64_t>((c + i) / 4) * ROWS] =
+                    make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+            }
+          }
+        }
+      }
+    } else if (__all_sync(0xffffffffu, ok)) {
       tc_after();
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
@@ -542,24 +647,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 32; ++i) v[i] = none ? 0.f : __uint_as_float(o[i]) * inv;
         if (have_row) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            // elements 0 .. 7 stand at 0 2 4 6 1 3 5 7
-            uint32_t w[4];
-            if (p.out_dt == OMQ_F16) {
-              w[0] = pack_h2(v[i], v[i + 2]);
-              w[1] = pack_h2(v[i + 4], v[i + 6]);
-              w[2] = pack_h2(v[i + 1], v[i + 3]);
-              w[3] = pack_h2(v[i + 5], v[i + 7]);
-            } else {
-              const int e0[4] = {0, 4, 1, 5}, e1[4] = {2, 6, 3, 7};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 q = __floats2bfloat162_rn(v[i + e0[k]], v[i + e1[k]]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&q);
-              }
-            }
-            dst[(c + i) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 32; i += 8) dst[(c + i) / 8] = out_eight(v + i, p.out_dt);
         }
       }
       if (p.lse && have_row)
@@ -651,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       uint32_t pg = 0;
       // lane i < 8 finds the page of cell i of tile j, a tile before its copy is issued
       auto look = [&](int j) {
-        const int ci = j * 8 + lane;
+        const int ci = key0 / kCell + j * 8 + lane;
         id = -1;
         if (lane < 8 && ci < n_cell) {
           pg = static_cast<uint32_t>(ci) / static_cast<uint32_t>(p.pool.cells);
@@ -661,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       if (nt > 0) look(0);
       for (int j = 0; j < nt; ++j) {
-        const int st = j % NR, ci = j * 8 + lane;
+        const int st = j % NR, ci = key0 / kCell + j * 8 + lane;
         if (j >= NR) ok = wait_for(sb + F::RE + 8 * st, (j / NR - 1) & 1, abort_flag, DEV_ERR_TMA_WAIT);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -717,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t cells = mask[rs];
-        const int left = vis_max - j * KT;                 // keys of the tile that anyone sees
+        const int left = vis_max - key0 - j * KT;          // keys of the tile that anyone sees
         // Steps of key t's K or V row. A key that is not there gets zeros. A NaN step is kept
         // out of V, where it would meet the zero weights of rows that do not see the key, and
         // put into K instead, whose scores are masked row by row.
@@ -771,36 +859,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+// o of the rows of items whose keys were shared: sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M),
+// M the largest m_i, in the parts' order. A block takes 64 rows of an item; a lane a row (the
+// parts' loads are contiguous), a warp every fourth 8 columns.
 template <int D>
-omq_status launch_tiles(const AttnParams& p, int min_rows, cudaStream_t st) {
-  using F = TilesCfg<D>;
+__global__ void __launch_bounds__(256) kv_tiles_join_kernel(AttnParams p, int pieces, TilesSpace ws) {
+  pdl_wait();
+  pdl_launch();
+  const int item = blockIdx.x / (ROWS / 64), g = blockIdx.x % (ROWS / 64);
+  const int2 at = ws.desc[item];
+  if (at.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = item % p.pool.Hkv, r = g * 64 + (warp & 1) * 32 + lane;
+  const int first = p.cu[at.x];
+  const int n_new = min(max(p.cu[at.x + 1] - first, 0), p.max_q);
+  const int row = at.y * ROWS + r, tok = row / p.G, hq = kvh * p.G + row - tok * p.G;
+  if (tok >= n_new || first + tok >= p.T) return;
+  const float2* ml = ws.ml + static_cast<int64_t>(item) * pieces * ROWS + r;
+  float M = -INFINITY;
+  for (int i = 0; i < pieces; ++i) M = fmaxf(M, ml[static_cast<int64_t>(i) * ROWS].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  constexpr int CH = D / 32;                               // groups of 8 columns of a warp
+  float l = 0.f, o[CH][8] = {};
+  const float4* src = ws.o + static_cast<int64_t>(item) * pieces * (D / 4) * ROWS + r;
+#pragma unroll 2
+  for (int i = 0; i < pieces; ++i) {
+    const float2 t = ml[static_cast<int64_t>(i) * ROWS];
+    if (t.y == 0.f) continue;                              // no key (a NaN sum goes on)
+    const float f = ex2((t.x == -INFINITY ? 0.f : t.x) - ref);
+    l += t.y * f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 x = src[(static_cast<int64_t>(i) * (D / 4) + 2 * ((warp >> 1) + 4 * c) + k) * ROWS];
+        o[c][4 * k] += x.x * f;
+        o[c][4 * k + 1] += x.y * f;
+        o[c][4 * k + 2] += x.z * f;
+        o[c][4 * k + 3] += x.w * f;
+      }
+    }
+  }
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  const int64_t orow = static_cast<int64_t>(first + tok) * p.Hq + hq;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[c][k] *= inv;
+    dst[(warp >> 1) + 4 * c] = out_eight(o[c], p.out_dt);
+  }
+  if (p.lse && warp < 2) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (ref + __log2f(l));
+}
+
+// How a launch is laid out; the workspace depends on it.
+struct TilesPlan {
+  int64_t list;        // row tiles of all requests, at most
+  int64_t items;       // the same of all kv heads
+  int pieces;          // pairs that share an item's keys
+};
+TilesPlan plan_tiles(const AttnParams& p, int min_rows) {
+  TilesPlan r;
+  const int64_t most = ceil_div(static_cast<int64_t>(p.max_q) * p.G, ROWS) * p.n_req;
+  // the requests' rows are at most T G: so many full tiles, and one more of each request that
+  // has enough rows
+  const int64_t rows = p.T * p.G;
+  const int64_t reqs = min_rows > 0 && rows / min_rows < p.n_req ? rows / min_rows : p.n_req;
+  r.list = rows / ROWS + reqs < most ? rows / ROWS + reqs : most;
+  r.items = r.list * p.pool.Hkv;
+  const int64_t pairs = num_sms() / 2;
+  const int64_t keys = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, KT);
+  // Estimated microseconds: 2 a tile of keys, 8 to begin and end a part, 6 for the join. One
+  // request of 4096 tokens, 32 kv heads, 512 rows: 2 parts 54, whole 77; 2 requests of 8 kv heads,
+  // 1024 rows: 2 parts 59, whole 82; 4 of 1024 tokens, 1024 rows: whole 36.
+  int64_t best = 0;
+  r.pieces = 1;
+  for (int64_t n = 1; n <= 64 && (n == 1 || (n <= keys && n * r.items <= 3 * pairs)); ++n) {
+    const int64_t us = ceil_div(n * r.items, pairs) * (2 * ceil_div(keys, n) + 8) + (n > 1 ? 6 : 0);
+    if (n == 1 || us < best) {
+      best = us;
+      r.pieces = static_cast<int>(n);
+    }
+  }
+  return r;
+}
+template <int D>
+size_t space_of(const TilesPlan& r, void* base, TilesSpace* ws) {
+  if (r.pieces == 1) return 0;
+  const size_t parts = static_cast<size_t>(r.items) * r.pieces;
+  const size_t o = parts * ROWS * D * 4, ml = parts * ROWS * 8;
+  if (ws) {
+    ws->o = static_cast<float4*>(base);
+    ws->ml = reinterpret_cast<float2*>(static_cast<char*>(base) + o);
+    ws->desc = reinterpret_cast<int2*>(static_cast<char*>(base) + o + ml);
+  }
+  return o + ml + static_cast<size_t>(r.items) * sizeof(int2);
+}
+
+template <int D, bool SPLIT>
+omq_status ready_on(int dev) {
   static thread_local int ready = -1;
+  if (ready == dev) return OMQ_OK;
+  cudaError_t e = cudaFuncSetAttribute(kv_tiles_kernel<D, SPLIT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, TilesCfg<D>::SMEM);
+  cudaFuncAttributes fa = {};
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kv_tiles_kernel<D, SPLIT>);
+  if (e != cudaSuccess) {
+    set_cuda_error(e);
+    return OMQ_ERR_CUDA;
+  }
+  // the softmax warps' larger share would wait for registers that were never allocated
+  if (fa.numRegs < REGS) return OMQ_ERR_UNSUPPORTED;
+  ready = dev;
+  return OMQ_OK;
+}
+
+template <int D>
+omq_status launch_tiles(const AttnParams& p, int min_rows, void* space, cudaStream_t st) {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (ready != dev) {
-    cudaError_t e = cudaFuncSetAttribute(kv_tiles_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
-    cudaFuncAttributes fa = {};
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kv_tiles_kernel<D>);
-    if (e != cudaSuccess) {
-      set_cuda_error(e);
-      return OMQ_ERR_CUDA;
-    }
-    // the softmax warps' larger share would wait for registers that were never allocated
-    if (fa.numRegs < REGS) return OMQ_ERR_UNSUPPORTED;
-    ready = dev;
+  const TilesPlan r = plan_tiles(p, min_rows);
+  TilesSpace ws = {};
+  space_of<D>(r, space, &ws);
+  const omq_status s = r.pieces > 1 ? ready_on<D, true>(dev) : ready_on<D, false>(dev);
+  if (s != OMQ_OK) return s;
+  const dim3 grid(static_cast<unsigned>(2 * r.items * r.pieces));
+  if (r.pieces > 1) {
+    launch_k(kv_tiles_kernel<D, true>, grid, THREADS, TilesCfg<D>::SMEM, st, p, r.pieces, min_rows, ws);
+    launch_k(kv_tiles_join_kernel<D>, dim3(static_cast<unsigned>(r.items * (ROWS / 64))), 256, 0, st, p,
+             r.pieces, ws);
+  } else {
+    launch_k(kv_tiles_kernel<D, false>, grid, THREADS, TilesCfg<D>::SMEM, st, p, 1, min_rows, ws);
   }
-  const int64_t tiles = ceil_div(static_cast<int64_t>(p.max_q) * p.G, 512);
-  const int64_t items = tiles * p.pool.Hkv * p.n_req;
-  launch_k(kv_tiles_kernel<D>, dim3(static_cast<unsigned>(2 * items)), THREADS, F::SMEM, st, p,
-           static_cast<int>(tiles), min_rows);
   return launch_status();
 }
 
 }  // namespace
 
-omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, cudaStream_t st) {
-  return D == 128 ? launch_tiles<128>(p, min_rows, st) : launch_tiles<64>(p, min_rows, st);
+size_t attn_tiles_space(const AttnParams& p, int64_t D, int min_rows) {
+  const TilesPlan r = plan_tiles(p, min_rows);
+  return D == 128 ? space_of<128>(r, nullptr, nullptr) : space_of<64>(r, nullptr, nullptr);
+}
+
+omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, void* space, cudaStream_t st) {
+  return D == 128 ? launch_tiles<128>(p, min_rows, space, st) : launch_tiles<64>(p, min_rows, space, st);
 }
 
 }  // namespace kv

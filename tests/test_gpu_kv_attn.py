@@ -255,3 +255,69 @@ def test_pool_beyond_32_bit_byte_offsets(omq, cuda_device):
         table = torch.where(s.args[2] >= 0, s.args[2] + (n_pages - n), s.args[2]).int()
         got = omq.kv_attn(s.args[0], big, table, s.args[3], s.args[4], s.max_q)
         assert torch.equal(got, omq.kv_attn(*s.args, s.max_q))
+
+
+@pytest.mark.parametrize("D,G,dt", [(128, 4, "bf16"), (64, 2, "f16"), (128, 1, "f16")])
+def test_requests_of_64_and_65_rows(omq, cuda_device, D, G, dt):
+    """Both sides of the row count at which a request changes its kernel, together in one call;
+    G = 4 has no request of 65 rows, but of 64 and 68."""
+    s = Setup(cuda_device, [700, 65, 1200, 66, 90], [64 // G, 64 // G + 1, 64 // G + 1, 64 // G, 1], 2, G, D, 16, dt,
+              seed=37 + G)
+    for causal in (True, False):
+        out, lse = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
+        omq.sync_check()
+        s.check(out, lse, causal, rows=9)
+
+
+@pytest.mark.parametrize("lens,new,Hkv,G,D", [
+    ([5000], [300], 1, 2, 128),          # one request: its keys shared by many pairs
+    ([2600, 140, 2500], [260, 140, 1], 1, 2, 64),
+    ([4097, 0, 130], [80, 0, 130], 2, 1, 128),
+    ([900, 1300], [700, 1100], 1, 1, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_keys_shared_between_pairs(omq, cuda_device, lens, new, Hkv, G, D, causal):
+    """Few row tiles under long contexts; a request far shorter than the table, whose later
+    shares are empty; first rows that see only the first shares. Twice, to the bit."""
+    s = Setup(cuda_device, lens, new, Hkv, G, D, 32, "bf16", seed=41)
+    out, lse = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
+    again, lse2 = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
+    omq.sync_check()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    s.check(out, lse, causal, rows=83)
+
+
+def test_shared_keys_missing_pages_nan_and_empty_rows(omq, cuda_device):
+    """More queries than keys in a request whose keys are shared; pages that are not there make
+    whole shares empty; a NaN key in the last share reaches only the rows that see it."""
+    s = Setup(cuda_device, [4000, 30], [200, 200], 1, 1, 128, 16, "f16", seed=43)
+    hidden = [(0, p) for p in range(40, 200)]
+    for b, p in hidden:
+        s.args[2][b, p] = -1
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse, hidden=hidden, rows=29)
+    assert not out[200:370].any() and bool((lse[200:370] == -np.inf).all())
+    page, off = divmod(3950, 16)
+    cell = s.pool[s.table[0, page], 0, 0]
+    cell[2 * kc.CELL * 64 + 4 * off: 2 * kc.CELL * 64 + 4 * off + 4] = 255
+    bad = omq.kv_attn(*s.args, s.max_q)
+    omq.sync_check()
+    first = 3950 - (4000 - 200)
+    assert bool(torch.isnan(bad[first:200]).all())
+    assert torch.equal(bad[:first], out[:first]) and torch.equal(bad[200:], out[200:])
+
+
+@pytest.mark.parametrize("n_req", [40, 600, 1100])
+def test_one_chunk_among_many_single_tokens(omq, cuda_device, n_req):
+    """A step of a serving batch: single tokens, two chunks at any place of the batch (found
+    over several rounds of the block's scan), requests without new tokens."""
+    rng = np.random.default_rng(n_req)
+    lens = rng.integers(1, 40, n_req)
+    new = rng.integers(0, 2, n_req)
+    for at, (n, m) in zip((n_req // 3, n_req - 1), ((700, 90), (260, 150))):
+        lens[at], new[at] = n, m
+    s = Setup(cuda_device, lens.tolist(), new.tolist(), 1, 1, 64, 16, "bf16", seed=47, extra_rows=5)
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    n = int(s.cu[-1])
+    s.check(out[:n], lse[:n], rows=37)
