@@ -20,7 +20,7 @@
 // kept in both operands (Q is staged in the same order) and undone where o is written.
 // Where the items are few for the 74 pairs, a pair takes an equal share of an item's keys and
 // leaves o and (m, l) in float32; a second kernel joins the parts in their order (one request
-// under 65536 tokens, 8 x 4 heads: 64 new tokens 950 -> 130 us, 512 new ones 1019 -> 527).
+// under 65536 tokens, 8 x 4 heads: 64 new tokens 949 -> 130 us, 128 new ones 1019 -> 141).
 // Which item a pair has follows from the lengths on the device, so that requests of another
 // kind (a step with one chunk and many single tokens) take no pairs.
 // Warp roles (512 threads; registers are shared out again at the start, 200 a softmax thread
@@ -932,11 +932,18 @@ TilesPlan plan_tiles(const AttnParams& p, int min_rows) {
   const int64_t keys = ceil_div(static_cast<int64_t>(p.width) * p.pool.page, KT);
   // Estimated microseconds: 2 a tile of keys, 8 to begin and end a part, 6 for the join. One
   // request of 4096 tokens, 32 kv heads, 512 rows: 2 parts 54, whole 77; 2 requests of 8 kv heads,
-  // 1024 rows: 2 parts 59, whole 82; 4 of 1024 tokens, 1024 rows: whole 36.
+  // 1024 rows: 2 parts 59, whole 82; 4 of 1024 tokens, 1024 rows: whole 36. Several requests may
+  // be as long as each other or, as likely, spread evenly below the longest, when shares even
+  // out the pairs: 33 requests of up to 53063 tokens, 2 kv heads, 33 x 4 rows: 3 parts 556, whole
+  // 804 (of 20000 tokens each: 339, whole 309).
   int64_t best = 0;
   r.pieces = 1;
   for (int64_t n = 1; n <= 64 && (n == 1 || (n <= keys && n * r.items <= 3 * pairs)); ++n) {
-    const int64_t us = ceil_div(n * r.items, pairs) * (2 * ceil_div(keys, n) + 8) + (n > 1 ? 6 : 0);
+    const int64_t part = ceil_div(keys, n), longest = 2 * part + 8;
+    const int64_t equal = ceil_div(n * r.items, pairs) * longest;
+    const int64_t mean = n * r.items * (part + 8) / pairs + longest / 2;
+    const int64_t spread = p.n_req == 1 ? equal : mean > longest ? mean : longest;
+    const int64_t us = equal + spread + (n > 1 ? 12 : 0);
     if (n == 1 || us < best) {
       best = us;
       r.pieces = static_cast<int>(n);
