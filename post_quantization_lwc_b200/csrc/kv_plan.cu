@@ -10,6 +10,7 @@
 // offsets, and all its blocks write the token maps, each token finding its request by
 // bisection over the offsets in shared memory. A few microseconds of dependent loads and
 // barriers, whatever the size; bandwidth plays no part below some hundred thousand tokens.
+// Measured: 8 decoding requests 6.6 us, 256 mixed ones with 16,000 new tokens 13.3 us.
 #include "kv_internal.cuh"
 
 namespace omq {

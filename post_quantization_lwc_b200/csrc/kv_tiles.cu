@@ -29,6 +29,12 @@
 //   8, 9      expand K; 10, 11 expand V
 //   12        MMA issue (leader CTA); TMEM allocation
 //   13        bulk copies of the raw cells
+// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 537 us (1.02 PFLOP/s), three chunks of up
+// to 1000 behind contexts of up to 16411 566 us (0.91); 32 heads, 2048 tokens 69 us (0.50: 4 to 16
+// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3800 cycles against
+// 2048 of products and another 2048 of exponentials (256 rows x 128 keys a CTA, 16 a clock); the
+// two meet only partly, a row's chain being read S, maximum, exponentials, write P with no more
+// than two subtiles in 512 columns of tensor memory. Tensor cores 52% busy, exponential unit 53%.
 // Every mbarrier wait is bounded; on expiry the error flag is raised, every role stops, copies
 // and MMAs in flight are drained and both CTAs meet before TMEM is released. Loads never
 // multicast.
