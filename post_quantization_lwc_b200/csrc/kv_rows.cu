@@ -8,7 +8,7 @@
 //   o             = (sum_j w_j cv_jd - sum_j w_j zv_j) / sum_j (w_j / hv_j)
 // so w_j = p_j hv_j up to the row's common factor lies in [0, 1] for any hv and its rounding to
 // float16 (the operand; the same rounded value weighs zv_j) is relative to the largest
-// contribution. A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
+// contribution (zero points far from the codes: see kFarZ). A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
 // second nibble of a 16-bit lane: one AND makes two operands, exact, and the powers of two go
 // into q (the odd nibbles' q times 1/16; the tile's q scaled by a power of two, so both input
 // types are exact but for values 2^-28 below the tile's largest) and into the result.
@@ -52,6 +52,10 @@ namespace {
 constexpr int STEP = 64;              // tokens of a run: four cells
 constexpr int NCELL = STEP / kCell;
 constexpr int STAGES = 2;
+// Zero points beyond this are weighed by the float32 weight, not the float16 one: a constant row
+// of 5 is 0 + 5e8 steps of 1e-8, and its weight, p 1e-8 beside another token's p 0.1, is below
+// float16's numbers. The rounded weight then meets only codes (0 .. 15, less than |c - z|).
+constexpr float kFarZ = 64.f;
 constexpr int W = 4;                  // warps of a block
 
 template <int D, int NB>
@@ -464,6 +468,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
       // (j, g) = 2 j + (g & 1) of cell g / 2, entry 8 j + g, in place of the cells' steps. A
       // token that is not there has no weight and finite steps; a NaN step of V is put into K's,
       // so that it reaches the rows that see the token, and only those.
+      bool far = false;                                    // a value row far from zero
       {
         float4 mt[2];
 #pragma unroll
@@ -478,8 +483,9 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           mt[i].y = kh * kz;
           mt[i].z = bad ? 0.f : lg2(vh);
           mt[i].w = there ? static_cast<float>(lds_i(a + 192)) : 0.f;
+          far = far || fabsf(mt[i].w) > kFarZ;
         }
-        __syncwarp();
+        far = __any_sync(0xffffffffu, far);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int en = lane + 32 * i;
@@ -595,6 +601,17 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           zs[nb][0] = __fmaf_rn(wr.x, vz[j], zs[nb][0]);
           zs[nb][1] = __fmaf_rn(wr.y, vz[j], zs[nb][1]);
           pw[nb][j >> 1][j & 1] = movm_t(wh);
+        }
+        if (far) {                                         // warp-uniform
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float w0 = ex2(x[nb][j].x - ref0), w1 = ex2(x[nb][j].y - ref1);
+            const uint32_t wh = h2(w0, w1);
+            const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&wh));
+            const float z = fabsf(vz[j]) > kFarZ ? vz[j] : 0.f;
+            zs[nb][0] = __fmaf_rn(w0 - wr.x, z, zs[nb][0]);
+            zs[nb][1] = __fmaf_rn(w1 - wr.y, z, zs[nb][1]);
+          }
         }
       }
       // ---- o^T += V^T w: V's 8 x 8 blocks transposed on their way to registers

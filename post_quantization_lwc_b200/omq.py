@@ -423,15 +423,12 @@ def kv_pool(n_pages, Hkv, D, page, device="cuda") -> torch.Tensor:
                        device=device)
 
 
-def _on(device, stream, entry, args, *rest):
-    """Calls a cache entry point on the tensors' device and on `stream` (default: the device's
-    current one); raises for a status that is not OK. These calls last a few microseconds, so
-    the device is switched only where it is not the current one."""
+def _on(device, entry, args, *rest):
+    """Calls a cache entry point on the tensors' device and its current stream; raises for a
+    status that is not OK. These calls last a few microseconds, so the device is switched only
+    where it is not the current one."""
     index = device.index
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        raw = stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(index)
     if index == torch._C._cuda_getDevice():
         status = entry(args, *rest, raw)
     else:
@@ -439,6 +436,14 @@ def _on(device, stream, entry, args, *rest):
             status = entry(args, *rest, raw)
     if status != 0:
         raise OmqError(status, entry.__name__)
+
+
+def _with(stream, device):
+    """A call with ``stream`` runs as under torch.cuda.stream(stream): what it allocates (results,
+    workspace) is then that stream's memory, never a block that another stream still uses."""
+    if stream.device != device:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
 def _pool(pool) -> KvPool:
@@ -471,8 +476,11 @@ def _rows(device, t, shape, D):
 
 def rope_table(n_pos, D, base=10000.0, device="cuda", stream=None) -> torch.Tensor:
     """omq_rope_table: float32 [2, n_pos, D/2], cos and sin of position * base^(-2i/D)."""
+    if stream is not None:
+        with _with(stream, stream.device if device == "cuda" else torch.device(device)):
+            return rope_table(n_pos, D, base, stream.device)
     t = torch.empty(2, n_pos, D // 2, dtype=torch.float32, device=device)
-    _on(t.device, stream, _lib.omq_rope_table, n_pos, D, float(base), t.data_ptr())
+    _on(t.device, _lib.omq_rope_table, n_pos, D, float(base), t.data_ptr())
     return t
 
 
@@ -482,6 +490,9 @@ def kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_plac
     free_pages are updated in place, lens and n_free with ``in_place`` (else new tensors).
     Returns dict(lens, n_free, cu, slots, positions, requests)."""
     dev = lens.device
+    if stream is not None:
+        with _with(stream, dev):
+            return kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_place)
     if not lens.is_cuda:
         raise ValueError("tensors must be contiguous CUDA tensors")
     _ints(dev, lens, new_tokens, table, free_pages, n_free)
@@ -502,7 +513,7 @@ def kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_plac
                    after if own else lens.data_ptr(),
                    after + 4 * B if own else n_free.data_ptr(), at, maps, maps + 4 * capacity,
                    maps + 8 * capacity, capacity)
-    _on(dev, stream, _lib.omq_kv_plan, ctypes.byref(a))
+    _on(dev, _lib.omq_kv_plan, ctypes.byref(a))
     cu, slots, positions, requests, l, f = buf.split_with_sizes(
         (B + 1, capacity, capacity, capacity, own * B, own))
     return {"lens": l if own else lens, "n_free": f if own else n_free, "cu": cu, "slots": slots,
@@ -513,6 +524,10 @@ def kv_append(pool, slots, k, v, q=None, positions=None, rope=None, s_a=None, s_
               delta_o=None, abits=16, q_dtype=torch.float16, q_out=None, stream=None):
     """omq_kv_append: k, v [T, Hkv, D] (token stride free) rotated, scaled, quantized to 4 bits
     and stored at slots [T]. With q [T, Hq, D]: returns q~ [T, Hq, D] (into q_out if given)."""
+    if stream is not None:
+        with _with(stream, pool.device):
+            return kv_append(pool, slots, k, v, q, positions, rope, s_a, s_o, delta_o, abits,
+                             q_dtype, q_out)
     P = _pool(pool)
     D, Hkv, dev = P.D, P.Hkv, pool.device
     _ints(dev, slots)
@@ -554,19 +569,22 @@ def kv_append(pool, slots, k, v, q=None, positions=None, rope=None, s_a=None, s_
         raise ValueError("q_out without q")
     a = KvAppendArgs(P, T, Hq, _dt(dt), qp, k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld,
                      slots.data_ptr(), pos, rp, n_pos, sa, so, do, abits, qo, qdt)
-    _on(dev, stream, _lib.omq_kv_append, ctypes.byref(a))
+    _on(dev, _lib.omq_kv_append, ctypes.byref(a))
     return q_out
 
 
 def kv_read(pool, slots, dtype=torch.float32, stream=None):
     """omq_kv_read: the stored (k, v), each [T, Hkv, D], of the slots."""
+    if stream is not None:
+        with _with(stream, pool.device):
+            return kv_read(pool, slots, dtype)
     P = _pool(pool)
     dev = pool.device
     _ints(dev, slots)
     T = slots.numel()
     kv = torch.empty(2, T, P.Hkv, P.D, dtype=dtype, device=dev)
     at = kv.data_ptr()
-    _on(dev, stream, _lib.omq_kv_read, ctypes.byref(P), T, slots.data_ptr(), at,
+    _on(dev, _lib.omq_kv_read, ctypes.byref(P), T, slots.data_ptr(), at,
         at + kv.element_size() * T * P.Hkv * P.D, _dt(dtype))
     return kv.unbind(0)
 
@@ -576,6 +594,9 @@ def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, 
     """omq_kv_attn: attention of q [T, Hq, D] (the requests' rows per cu) over the cache; rows
     of a new `out` behind the last request are not written. Returns out [T, Hq, D], or
     (out, lse [T, Hq]) with ``lse``."""
+    if stream is not None:
+        with _with(stream, pool.device):
+            return kv_attn(q, pool, table, lens, cu, max_q, scale, causal, out, out_dtype, lse)
     P = _pool(pool)
     dev, D = pool.device, P.D
     _ints(dev, table, lens, cu)
@@ -596,7 +617,7 @@ def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, 
     ref = ctypes.byref(a)
     n = _lib.omq_kv_attn_workspace_bytes(ref)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _on(dev, stream, _lib.omq_kv_attn, ref, None if ws is None else ws.data_ptr(), n)
+    _on(dev, _lib.omq_kv_attn, ref, None if ws is None else ws.data_ptr(), n)
     return (out, ls) if lse else out
 
 

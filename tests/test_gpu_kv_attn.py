@@ -78,7 +78,7 @@ class Setup:
             m[p, :, cell, r] = x[..., 0].astype(t)
             pool[..., a:a + 64] = m.view(np.uint8).reshape(*pool.shape[:3], 64)
 
-    def check(self, out, lse=None, causal=True, scale=None, rows=None, hidden=()):
+    def check(self, out, lse=None, causal=True, scale=None, rows=None, hidden=(), far=None):
         """Every row (or every `rows`-th of a request) of every head against the statement.
         hidden: (request, page index) pairs whose table entries are not pages."""
         scale = self.D ** -0.5 if scale is None else scale
@@ -102,7 +102,7 @@ class Setup:
                     kh = h // self.G
                     (a, ah, az), (c, ch, cz) = self.kv[b]
                     o, l, tol, ltol = kc.attend(self.q[t, h].double().numpy(), a[:, kh], ah[:, kh], az[:, kh],
-                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps, step[b])
+                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps, step[b], far)
                     err = np.abs(got[t, h] - o)
                     assert np.all(err <= tol), (b, i, h, float((err - tol).max()), float(err.max()))
                     worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()))
@@ -321,3 +321,85 @@ def test_one_chunk_among_many_single_tokens(omq, cuda_device, n_req):
     omq.sync_check()
     n = int(s.cu[-1])
     s.check(out[:n], lse[:n], rows=37)
+
+
+@pytest.mark.parametrize("n,new,G,D,dt", [(70, 1, 4, 128, "bf16"), (300, 1, 1, 64, "f16"), (150, 9, 2, 128, "f16"),
+                                          (200, 90, 1, 128, "bf16"), (900, 1, 4, 128, "f16")])
+def test_constant_value_rows_among_others(omq, cuda_device, n, new, G, D, dt):
+    """Value rows that are constant, or nearly, have steps of 1e-8 and zero points of up to 2^30:
+    beside ordinary rows their weights are below float16's, their values are not."""
+    s = Setup(cuda_device, [n, n - 1], [new, new], 1, G, D, 16, dt, seed=53)
+    rng = np.random.default_rng(53)
+    for b, m in enumerate(s.lens):
+        pos = np.arange(b, m, 5)
+        x = np.broadcast_to(rng.choice([5.0, -3.0, 0.25, 8.0, -0.001], (len(pos), 1, 1)), (len(pos), 1, D))
+        x = (x + rng.choice([0.0, 2e-6, 1e-4], (len(pos), 1, 1)) * rng.standard_normal((len(pos), 1, D))).astype(np.float32)
+        c, h, z = kc.encode(x)
+        for have, got in zip(s.kv[b][1], (c, h, z)):
+            have[pos] = got
+        s.put(s.pool_np, s.table[b, pos // 16] * 16 + pos % 16, 1, c, h, z)
+    s.pool.copy_(torch.from_numpy(s.pool_np))
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse, rows=11, far=64)
+
+
+def test_side_stream_owns_what_the_call_allocates(omq, cuda_device):
+    """With stream=, results and workspace belong to that stream: while the current stream is
+    busy with memory it has already given back, calls on the side stream do not get that memory."""
+    s = Setup(cuda_device, [5000, 3000, 900], [3, 3, 3], 2, 4, 128, 64, "bf16", seed=59)
+    want = omq.kv_attn(*s.args, s.max_q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        busy = [torch.empty(1 << 20, device=cuda_device) for _ in range(12)]
+        torch.cuda._sleep(2_000_000)
+        for t in busy:
+            t.fill_(float("nan"))
+        del t, busy                                         # still being written by this stream
+        got = [omq.kv_attn(*s.args, s.max_q, stream=side) for _ in range(3)]
+        side.synchronize()
+        assert all(torch.equal(g, want) for g in got)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want) for g in got)
+
+
+def test_two_streams_at_once(omq, cuda_device):
+    """Calls that overlap on two streams, single tokens and chunks with shared keys, each with its
+    own workspace: the results of the same calls alone."""
+    a = Setup(cuda_device, [9000, 5000], [1, 4], 2, 4, 128, 64, "bf16", seed=61)
+    b = Setup(cuda_device, [6000, 700], [200, 300], 2, 4, 128, 64, "bf16", seed=67)
+    want = [omq.kv_attn(*s.args, s.max_q) for s in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate((a, b)):
+            got[i].append(omq.kv_attn(*s.args, s.max_q, stream=streams[i]))
+    torch.cuda.synchronize()
+    omq.sync_check()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+
+
+def test_captured_chunks_and_a_second_graph(omq, cuda_device):
+    """Chunks with shared keys captured twice in two graphs, replayed in turn while eager calls run
+    between them; lengths and queries change between replays."""
+    s = Setup(cuda_device, [4000, 300], [200, 100], 1, 2, 128, 16, "f16", seed=71)
+    lens = s.args[3].clone()
+    graphs, outs = [], []
+    omq.kv_attn(*s.args, s.max_q)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(omq.kv_attn(s.args[0], s.args[1], s.args[2], lens, s.args[4], s.max_q))
+        graphs.append(g)
+    for n in (4000, 3111, 200):
+        lens.copy_(torch.tensor([n, 300], dtype=torch.int32))
+        s.args[0].mul_(0.75)
+        want = omq.kv_attn(s.args[0], s.args[1], s.args[2], lens, s.args[4], s.max_q)
+        for g in graphs * 2:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    omq.sync_check()
