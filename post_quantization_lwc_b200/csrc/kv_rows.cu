@@ -468,7 +468,6 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
       // (j, g) = 2 j + (g & 1) of cell g / 2, entry 8 j + g, in place of the cells' steps. A
       // token that is not there has no weight and finite steps; a NaN step of V is put into K's,
       // so that it reaches the rows that see the token, and only those.
-      bool far = false;                                    // a value row far from zero
       {
         float4 mt[2];
 #pragma unroll
@@ -483,9 +482,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           mt[i].y = kh * kz;
           mt[i].z = bad ? 0.f : lg2(vh);
           mt[i].w = there ? static_cast<float>(lds_i(a + 192)) : 0.f;
-          far = far || fabsf(mt[i].w) > kFarZ;
         }
-        far = __any_sync(0xffffffffu, far);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int en = lane + 32 * i;
@@ -602,7 +599,10 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           zs[nb][1] = __fmaf_rn(wr.y, vz[j], zs[nb][1]);
           pw[nb][j >> 1][j & 1] = movm_t(wh);
         }
-        if (far) {                                         // warp-uniform
+        const float fz = max3(max3(fabsf(vz[0]), fabsf(vz[1]), fabsf(vz[2])),
+                              max3(fabsf(vz[3]), fabsf(vz[4]), fabsf(vz[5])),
+                              fmaxf(fabsf(vz[6]), fabsf(vz[7])));
+        if (__any_sync(0xffffffffu, fz > kFarZ)) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float w0 = ex2(x[nb][j].x - ref0), w1 = ex2(x[nb][j].y - ref1);
