@@ -598,12 +598,12 @@ omq_status omq_kv_plan(const omq_kv_plan_args* args, omq_stream_t stream);
  *   h = max((max - min) / 15, 1e-8), z = -round(min / h), c = clamp(round(x / h) + z, 0, 15)
  *   q_out = q~ in q_dt, or for abits < 16 its fake-quant with 2^abits - 1 in place of 15
  * A row holding a NaN or an infinity, or whose range overflows, is stored with h = NaN and
- * reads back as NaN. RoPE takes pairs (i, i + D/2) and row positions[t] of the table; no
+ * reads back as NaN; z is kept within +-2^30 (a constant row beyond 10.7 is cut there). RoPE takes pairs (i, i + D/2) and row positions[t] of the table; no
  * positions (or no table): no rotation. s_a, s_o, delta_o [Hkv, D] or NULL (no transform);
  * query head j shares those of kv head j / (Hq / Hkv).
  * q, k, v: [T, Hq or Hkv, D] in dt, a token's heads back to back, tokens q_ld / k_ld / v_ld
  * elements apart (slices of one fused product are fine; rows 16-byte aligned). q may be NULL.
- * q_out [T, Hq, D] dense. A token whose slot is outside the pool (-1 in particular) or whose
+ * q_out [T, Hq, D] dense, overlapping none of q, k, v (OMQ_ERR_UNSUPPORTED). A token whose slot is outside the pool (-1 in particular) or whose
  * position is outside the table is skipped: nothing stored, its row of q_out left as it was.
  * Two rows with the same slot leave that slot with either row's values, or some of each.
  * ------------------------------------------------------------------------------------ */
@@ -640,11 +640,15 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * q [T, Hq, D] F16 or BF16, tokens q_ld elements apart, rows 16-byte aligned; out [T, Hq, D]
  * dense, F16 or BF16; lse [T, Hq] float32 (natural log of the softmax's denominator) or NULL.
  * The codes are exact operands and sums, statistics and steps are float32; the weights are
- * rounded to float16 relative to the row's largest, q exactly unless an element is 2^-28 of
- * the largest of the rows it is processed with. For a request of more than 64 query rows per kv
- * head (rows = tokens x Hq / Hkv), k and v themselves are float16 operands, rounded once (so
- * |k scale log2 e| and |v| below 65504). Results are bitwise reproducible on one device.
- * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL).
+ * rounded to float16 (what is below 2^-39, with many rows 2^-31, of the row's largest is lost),
+ * q exactly unless an element is 2^-28 of the largest of the rows it is processed with. For a
+ * request of more than 64 query rows per kv head (rows = tokens x Hq / Hkv), k and v themselves
+ * are float16 operands, rounded once (so |k scale log2 e| and |v| below 65504, and |v| to no
+ * finer than 2^-25). Results are bitwise reproducible on one device. out and lse overlap nothing
+ * that is read (out over q: OMQ_ERR_UNSUPPORTED).
+ * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL), 16-byte aligned, from
+ * a query under the device of the call; its contents are nothing before and after. Calls (and
+ * graphs) that may run at the same time need one each.
  * ------------------------------------------------------------------------------------ */
 typedef struct {
   omq_kv_pool pool;

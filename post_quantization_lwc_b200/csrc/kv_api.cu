@@ -37,6 +37,11 @@ omq_status check_rows(const void* p, int64_t ld, int64_t heads, int64_t D, omq_d
   return OMQ_OK;
 }
 
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uint64_t>(nb) && y < x + static_cast<uint64_t>(na);
+}
+
 #define KV_TRY(expr)                  \
   do {                                \
     omq_status _s = (expr);           \
@@ -58,6 +63,9 @@ omq_status check_attn(const omq_kv_attn_args* a) {
   if ((rows / 8 + 1) * a->pool.Hkv >= (int64_t{1} << 27) / a->n_req) return OMQ_ERR_SHAPE;
   KV_TRY(check_rows(a->q, a->q_ld, a->Hq, a->pool.D, a->dt));
   if (!aligned16(a->out)) return OMQ_ERR_ALIGN;
+  // q is read by several blocks, some after others have written out
+  const int64_t row = a->Hq * a->pool.D * 2;
+  if (overlap(a->q, 2 * (a->T - 1) * a->q_ld + row, a->out, a->T * row)) return OMQ_ERR_UNSUPPORTED;
   return OMQ_OK;
 }
 
@@ -147,6 +155,14 @@ omq_status omq_kv_append(const omq_kv_append_args* a, omq_stream_t stream) {
   }
   const int64_t rows = (a->q ? a->Hq : 0) + 2 * a->pool.Hkv;
   if (a->T > (int64_t{1} << 31) / rows) return OMQ_ERR_SHAPE;
+  if (a->q) {                                              // other blocks still read these
+    const int64_t es = esize(a->dt), kv = a->pool.Hkv * a->pool.D, qw = a->Hq * a->pool.D;
+    const int64_t n = a->T * qw * esize(a->q_dt), last = a->T - 1;
+    if (overlap(a->q, es * (last * a->q_ld + qw), a->q_out, n) ||
+        overlap(a->k, es * (last * a->k_ld + kv), a->q_out, n) ||
+        overlap(a->v, es * (last * a->v_ld + kv), a->q_out, n))
+      return OMQ_ERR_UNSUPPORTED;
+  }
   kv::AppendParams p{};
   p.pool = view(a->pool);
   p.T = a->T;

@@ -4,9 +4,9 @@
 // o = sum_j p_j v_j with p = softmax_j(scale q . k_j), k_j = (c - z) h and v_j alike. The codes
 // themselves are the matrix instructions' operands and the steps stay outside, in binary32:
 //   q . k_j       = h_j (sum_d q_d c_jd - z_j sum_d q_d)
-//   x_j           = scale log2(e) q . k_j + log2 hv_j,   w_j = 2^(x_j - max x)
+//   x_j           = scale log2(e) q . k_j + log2 hv_j,   w_j = 2^(x_j - max x + 15)
 //   o             = (sum_j w_j cv_jd - sum_j w_j zv_j) / sum_j (w_j / hv_j)
-// so w_j = p_j hv_j up to the row's common factor lies in [0, 1] for any hv and its rounding to
+// so w_j = p_j hv_j up to the row's common factor lies in [0, 2^15] for any hv and its rounding to
 // float16 (the operand; the same rounded value weighs zv_j) is relative to the largest
 // contribution (zero points far from the codes: see kFarZ). A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
 // second nibble of a 16-bit lane: one AND makes two operands, exact, and the powers of two go
@@ -56,6 +56,9 @@ constexpr int STAGES = 2;
 // of 5 is 0 + 5e8 steps of 1e-8, and its weight, p 1e-8 beside another token's p 0.1, is below
 // float16's numbers. The rounded weight then meets only codes (0 .. 15, less than |c - z|).
 constexpr float kFarZ = 64.f;
+// The largest weight of a row is 2^15, near the top of float16: what falls below its smallest
+// number is then 2^-40 of the largest, and a long context's many small weights are kept.
+constexpr float kUp = 15.f;
 constexpr int W = 4;                  // warps of a block
 
 template <int D, int NB>
@@ -158,7 +161,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t orow, int
     packed = *reinterpret_cast<const uint32_t*>(&v);
   }
   *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = packed;
-  if (p.lse && d == 0) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
+  if (p.lse && d == 0) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (m + (__log2f(l) - kUp));
 }
 
 // Query rows of a request, and its runs per item (one without keys still writes its zeros).
@@ -569,6 +572,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
         m0 = fmaxf(m0, mx[nb][0]);
         m1 = fmaxf(m1, mx[nb][1]);
         const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+        const float up0 = ref0 - kUp, up1 = ref1 - kUp;
         const bool moved = m0 != mx[nb][0] || m1 != mx[nb][1];
         if (__any_sync(0xffffffffu, moved)) {
           const float al0 = ex2(mx[nb][0] - ref0), al1 = ex2(mx[nb][1] - ref1);
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float w0 = ex2(x[nb][j].x - ref0), w1 = ex2(x[nb][j].y - ref1);
+          const float w0 = ex2(x[nb][j].x - up0), w1 = ex2(x[nb][j].y - up1);
           const float rh = ex2(-lh[j]);                    // 1 / vh
           ls[nb][0] = __fmaf_rn(w0, rh, ls[nb][0]);
           ls[nb][1] = __fmaf_rn(w1, rh, ls[nb][1]);
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
         if (__any_sync(0xffffffffu, fz > kFarZ)) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float w0 = ex2(x[nb][j].x - ref0), w1 = ex2(x[nb][j].y - ref1);
+            const float w0 = ex2(x[nb][j].x - up0), w1 = ex2(x[nb][j].y - up1);
             const uint32_t wh = h2(w0, w1);
             const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&wh));
             const float z = fabsf(vz[j]) > kFarZ ? vz[j] : 0.f;

@@ -1,7 +1,7 @@
 // Attention of many query rows (prompts and their chunks) over the 4-bit paged cache on the
 // 5th-generation tensor cores (tcgen05, sm_100a).
 //
-//   x_ij = q_i . k'_j,  k'_j = scale log2(e) (c_j - z_j) hk_j;   w_ij = 2^(x_ij - m_i)
+//   x_ij = q_i . k'_j,  k'_j = scale log2(e) (c_j - z_j) hk_j;   w_ij = 2^(x_ij - m_i + 7)
 //   o_i  = sum_j w_ij v_j / sum_j w_ij,  v_j = (c_j - z_j) hv_j
 // k', v and w are float16 operands, each rounded once (relative 2^-12), as in the calibrated block's
 // own attention; statistics, sums and accumulators are float32. (Keeping the steps outside the
@@ -65,6 +65,7 @@ constexpr int THREADS = 512;
 constexpr int REGS = 128, REGS_SOFTMAX = 200, REGS_OTHER = 56;   // per thread: launch, after
 static_assert(2 * REGS >= REGS_SOFTMAX + REGS_OTHER, "the shares come out of the launch's registers");
 constexpr int ROWS = 512;             // query rows of a pair
+constexpr float UP = 7.f;             // weights are 2^(x - m_i + UP), at most 2^15 in float16
 constexpr float GROW = 8.f;           // growth of a row's maximum (log2) that moves m_i
 
 template <int D>
@@ -578,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      const float2 nref = make_float2(-ref, -ref);
+      const float2 nref = make_float2(UP - ref, UP - ref);
       float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -657,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       if (p.lse && have_row)
-        p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * ((m == -INFINITY ? 0.f : m) + __log2f(l));
+        p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * ((m == -INFINITY ? 0.f : m) + (__log2f(l) - UP));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
@@ -916,7 +917,7 @@ __global__ void __launch_bounds__(256) kv_tiles_join_kernel(AttnParams p, int pi
     for (int k = 0; k < 8; ++k) o[c][k] *= inv;
     dst[(warp >> 1) + 4 * c] = out_eight(o[c], p.out_dt);
   }
-  if (p.lse && warp < 2) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (ref + __log2f(l));
+  if (p.lse && warp < 2) p.lse[orow] = none ? -INFINITY : 0.6931471805599453f * (ref + (__log2f(l) - UP));
 }
 
 // How a launch is laid out; the workspace depends on it.

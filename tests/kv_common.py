@@ -137,7 +137,7 @@ def get(pool, page, slots, which):
 
 # ------------------------------------------------------------------------------ attention
 
-def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step, operand_half_step=0.0, far=None):
+def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step, operand_half_step=0.0, far=None, tiny=-25):
     """One query row in binary64 against N keys (codes [N, D], h, z [N, 1]; seen [N] booleans).
     Returns (o, lse, bound of |o|'s error, bound of lse's error).
 
@@ -151,6 +151,8 @@ def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step, operand_half_s
       operands (many rows) k and v themselves rounded to float16: relative 2^-11 of each and, for
               k, of scale sum |q| |k| in the score (2^-25 absolute, times 2^-22 of a second part)
       sums    N/16 + 64 float32 additions (the matrix unit's by 2^-22) of terms p h (c + |z|)
+      tiny    exponent of that absolute error: with the largest weight 2^15 instead of 1, -40;
+              with 2^7 (many rows) -32
       far     zero points beyond this are weighed by the float32 weight, so that the float16
               rounding meets only the code there
       output  half a step of its type."""
@@ -180,7 +182,7 @@ def attend(q, kc, kh, kz, vc, vh, vz, seen, scale, out_half_step, operand_half_s
     met = np.abs(vc - vz)
     if far is not None:
         met = np.where(np.abs(vz) > far, vc, met)
-    sub = 2.0 ** -25 * w.max() * met.sum(0)
+    sub = 2.0 ** tiny * w.max() * met.sum(0)
     acc = (n / 16 + 64) * 2.0 ** -22 * (w @ (vc + np.abs(vz)))
     bound = (2.0 ** -11 + operand_half_step + e_p) * (p @ np.abs(v)) + sub + acc
     if operand_half_step:

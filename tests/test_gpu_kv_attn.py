@@ -78,7 +78,7 @@ class Setup:
             m[p, :, cell, r] = x[..., 0].astype(t)
             pool[..., a:a + 64] = m.view(np.uint8).reshape(*pool.shape[:3], 64)
 
-    def check(self, out, lse=None, causal=True, scale=None, rows=None, hidden=(), far=None):
+    def check(self, out, lse=None, causal=True, scale=None, rows=None, hidden=(), far=None, tiny=-25):
         """Every row (or every `rows`-th of a request) of every head against the statement.
         hidden: (request, page index) pairs whose table entries are not pages."""
         scale = self.D ** -0.5 if scale is None else scale
@@ -102,7 +102,7 @@ class Setup:
                     kh = h // self.G
                     (a, ah, az), (c, ch, cz) = self.kv[b]
                     o, l, tol, ltol = kc.attend(self.q[t, h].double().numpy(), a[:, kh], ah[:, kh], az[:, kh],
-                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps, step[b], far)
+                                                c[:, kh], ch[:, kh], cz[:, kh], seen, scale, eps, step[b], far, tiny)
                     err = np.abs(got[t, h] - o)
                     assert np.all(err <= tol), (b, i, h, float((err - tol).max()), float(err.max()))
                     worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()))
@@ -403,3 +403,49 @@ def test_captured_chunks_and_a_second_graph(omq, cuda_device):
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for o in outs)
     omq.sync_check()
+
+
+@pytest.mark.parametrize("new,G,D,dt", [(1, 2, 128, "f16"), (5, 4, 64, "f16"), (90, 1, 128, "f16")])
+def test_many_weights_far_below_the_largest(omq, cuda_device, new, G, D, dt):
+    """One key that all queries prefer by 2^25.5 over each of 60000 others, whose weights sum to a
+    part of the result that float16 outputs show. The bound: the others' share of o may change
+    by what their scores and the rounding of their weights (the first one's is exact) allow,
+    (4 e_s + 2^-11) sum p_j |v_j - o|; the float32 sums, n/16 + 64 of terms p h (c + |z|); the
+    output's half step. Weights below float16's numbers would lose the whole share."""
+    n = 60000
+    s = Setup(cuda_device, [n], [new], 1, G, D, 64, dt, seed=73, shift=2.0)
+    rng = np.random.default_rng(73)
+    r0, r1 = rng.standard_normal((2, 1, 1, D)).astype(np.float32)
+    k = np.broadcast_to(r0, (n, 1, D)).copy()
+    k[7] = r1
+    v = np.full((n, 1, D), 2.0, np.float32) + rng.random((n, 1, D), np.float32)
+    v[7] -= 2.5
+    pos = np.arange(n)
+    for w, x in enumerate((k, v)):
+        rows = kc.encode(x)
+        s.put(s.pool_np, s.table[0, pos // 64] * 64 + pos % 64, w, *rows)
+        s.kv[0][w] = rows
+    d = kc.values(*s.kv[0][0])[:, 0]
+    d = d[7] - d[8]
+    s.q = torch.from_numpy(np.broadcast_to(d * (25.5 * np.log(2) * D ** 0.5 / (d @ d)), (new, G, D)).copy()).half()
+    s.args[0] = s.q.to(cuda_device)
+    s.pool.copy_(torch.from_numpy(s.pool_np))
+    out, lse = omq.kv_attn(*s.args, s.max_q, lse=True)
+    omq.sync_check()
+    s.check(out, lse, rows=31, far=64, tiny=-40 if new * G <= 64 else -32)
+    (a, ah, az), (c, ch, cz) = s.kv[0]
+    seen = pos <= n - new
+    o, _, _, ltol = kc.attend(s.q[0, 0].double().numpy(), a[:, 0], ah[:, 0], az[:, 0], c[:, 0], ch[:, 0], cz[:, 0],
+                              seen, D ** -0.5, 2.0 ** -12, 0.0 if new * G <= 64 else 2.0 ** -11)
+    val = kc.values(c, ch, cz)[seen, 0]
+    sc = kc.values(a, ah, az)[seen, 0] @ s.q[0, 0].double().numpy() * D ** -0.5
+    p = np.exp(sc - sc.max()) / np.exp(sc - sc.max()).sum()
+    rest = np.arange(len(p)) != 7
+    share = p[rest] @ np.abs(val[rest] - o)
+    sums = (n / 16 + 64) * 2.0 ** -22 * (p @ (ch * (c + np.abs(cz)))[seen, 0])
+    tol = (2 * ltol + 2.0 ** -11) * share + sums + 2.0 ** -11 * (np.abs(o) + share) + 2.0 ** -25
+    if new * G > 64:
+        tol = tol + 2.0 ** -11 * np.abs(val).max(0)       # v itself, rounded to float16
+    assert np.all(np.abs(out[0, 0].double().cpu().numpy() - o) <= tol)
+    if new * G <= 64:
+        assert np.median(share / tol) > 1.3               # the bound tells the share from nothing

@@ -165,3 +165,19 @@ def test_quantizer_statement_is_the_oracle_encoder():
     assert np.array_equal(c, want.codes) and np.array_equal(h, want.h)
     assert np.array_equal(z.astype(np.int32), want.z_i32)
     assert np.array_equal(kc.values(c, h, z, np.float32), want.deq)
+
+
+FAR = P + (1 << 30)
+
+
+@pytest.mark.parametrize("kw", [dict(out=P), dict(out=P + 2048 * 15 + 2032), dict(q=FAR, out=FAR - 16 * 2048 + 16)])
+def test_attn_refuses_out_over_q(omq, kw):
+    a = attn_args(omq, **kw)
+    assert omq._lib.omq_kv_attn(ctypes.byref(a), None, 0, None) == 8
+    assert omq._lib.omq_kv_attn_workspace_bytes(ctypes.byref(a)) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(q=FAR, k=FAR + 4096, v=FAR + 8192, q_out=FAR), dict(q_out=P + 512, q=FAR, v=FAR),
+                                dict(q_out=P + 512, q=FAR, k=FAR)])
+def test_append_refuses_q_out_over_its_inputs(omq, kw):
+    assert omq._lib.omq_kv_append(ctypes.byref(append_args(omq, **kw)), None) == 8
