@@ -29,12 +29,15 @@
 //   8, 9      expand K; 10, 11 expand V
 //   12        MMA issue (leader CTA); TMEM allocation
 //   13        bulk copies of the raw cells
-// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 537 us (1.02 PFLOP/s), three chunks of up
-// to 1000 behind contexts of up to 16411 566 us (0.91); 32 heads, 2048 tokens 69 us (0.50: 4 to 16
-// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3800 cycles against
+// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 515 us (1.07 PFLOP/s), three chunks of up
+// to 1000 behind contexts of up to 16411 537 us (0.96); 32 heads, 2048 tokens 65 us (0.53: 4 to 16
+// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3600 cycles against
 // 2048 of products and another 2048 of exponentials (256 rows x 128 keys a CTA, 16 a clock); the
 // two meet only partly, a row's chain being read S, maximum, exponentials, write P with no more
 // than two subtiles in 512 columns of tensor memory. Tensor cores 52% busy, exponential unit 53%.
+// (Steps of 64 keys with two places for each subtile's scores, so that the next are ready when
+// a row's weights are done, took 652 us for 537: the narrower products of Q and K pass at the
+// pace of the wide ones.)
 // Every mbarrier wait is bounded; on expiry the error flag is raised, every role stops, copies
 // and MMAs in flight are drained and both CTAs meet before TMEM is released. Loads never
 // multicast.
@@ -364,7 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcast, so that the roles' branches are known to be warp-uniform)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + F::ABORT);
   volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + F::MASK);
@@ -674,20 +678,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t k_lo = ((sb + F::K_OFF) >> 4) | kDescLead;
       const uint32_t v_lo = ((sb + F::V_OFF) >> 4) | kDescLead;
       bool ok = true;
-      int k_ready = -1, v_ready = -1;                      // the last stage waited for
       // step j: O += P V of tile j, then S = Q K^T of tile j + 1, subtile by subtile (one copy
       // of the code for both)
 #pragma unroll 1
-      for (int j = -1; j < nt && ok; ++j) {
+      for (int j = -1; j < nt; ++j) {
+        // both operands' stages first: the waits between a subtile's weights and its next scores
+        // are on its critical path (chunks of 1000 behind 16411: 552 -> 537 us)
+        if (j >= 0) ok = wait_for(sb + F::VF + 8 * (j % NS), (j / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
+        if (j + 1 < nt)
+          ok = ok && wait_for(sb + F::KF + 8 * ((j + 1) % NS), ((j + 1) / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_after();
 #pragma unroll 1
         for (int s = 0; s < 2 && ok; ++s) {
           const int my_nt = s ? nt1 : nt0;
           if (j >= 0 && j < my_nt) {
             const int st = j % NS;
-            if (v_ready < j) ok = wait_for(sb + F::VF + 8 * st, (j / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
-            v_ready = j;
-            ok = ok && wait_for(sb + F::PF + 8 * s, j & 1, abort_flag, DEV_ERR_MMA_WAIT);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, wait_for(sb + F::PF + 8 * s, j & 1, abort_flag, DEV_ERR_MMA_WAIT));
             if (!ok) break;
             tc_after();
             const uint32_t va = v_lo + st * (F::VST >> 4);
@@ -711,13 +719,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const int jn = j + 1;
           if (jn < my_nt) {
             const int st = jn % NS;
-            if (jn == 0) ok = wait_for(sb + F::QF + 8 * s, 0, abort_flag, DEV_ERR_MMA_WAIT);
-            if (k_ready < jn)
-              ok = ok && wait_for(sb + F::KF + 8 * st, (jn / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
-            k_ready = jn;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_after();
+            if (jn == 0) {
+              ok = __all_sync(0xffffffffu, wait_for(sb + F::QF + 8 * s, 0, abort_flag, DEV_ERR_MMA_WAIT));
+              if (!ok) break;
+              tc_after();
+            }
             const uint32_t qa = q_lo + s * (F::QSUB >> 4), ka = k_lo + st * (F::KST >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
