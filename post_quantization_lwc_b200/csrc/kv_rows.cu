@@ -21,12 +21,13 @@
 // run on its own: a ring of bulk copies (one per 16-token cell, which holds codes and steps
 // together), K as the 16 x 16 operand straight from 16-byte shared loads, V transposed by
 // ldmatrix, no barrier between warps. At the end of an item or part the warps join their (max,
-// sum, o) in a fixed order; an item cut between blocks leaves float32 partials in the workspace,
-// which a second kernel joins in the blocks' order.
+// sum, o) in a fixed order; an item shared by up to eight blocks is joined by them, a cluster,
+// through distributed shared memory, one cut otherwise leaves float32 partials in the workspace,
+// which a second kernel joins; in the blocks' order either way.
 //
-// Measured: 64 decoding requests of up to 8192 tokens, 8 x 4 heads of 128: 82 us (4.0 TB/s), one
-// of 131072 38 us (4.0 TB/s), 33 of up to 4001 with 5 drafted tokens, 4 x 2 heads of 64: 23 us, one
-// of 2049, 32 heads 10.8 us. Neither DRAM (49%) nor issue (52%) is full: the registers (168 a
+// Measured: 64 decoding requests of up to 8192 tokens, 8 x 4 heads of 128: 79 us (4.1 TB/s), one
+// of 131072 38 us (4.0 TB/s), 33 of up to 4001 with 5 drafted tokens, 4 x 2 heads of 64: 21 us, one
+// of 2049, 32 heads 10.5 us. Neither DRAM (49%) nor issue (52%) is full: the registers (168 a
 // thread) leave 12 warps an SM, each of which waits on its own chain of scores, weights and
 // products; of the two, loads alone took 70 us and arithmetic alone 84 of then 92.
 #include "kv_internal.cuh"
@@ -60,6 +61,7 @@ constexpr float kFarZ = 64.f;
 // number is then 2^-40 of the largest, and a long context's many small weights are kept.
 constexpr float kUp = 15.f;
 constexpr int W = 4;                  // warps of a block
+constexpr int kCluster = 8;           // blocks that join their shares of an item by themselves
 
 template <int D, int NB>
 struct RowsCfg {
@@ -202,10 +204,11 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, volatile int64_t* sm, i
 
 // pieces == 0: the blocks share the line of runs evenly. pieces > 0: an item has that many
 // blocks, each an equal share of its runs, at least one a warp (1: block i takes item i whole);
-// tiles per request and head as the host bounds them.
+// together: they are one cluster, which joins them itself. tiles per request and head as the
+// host bounds them.
 template <int D, int NB>
 __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
-    kv_rows_kernel(AttnParams p, int tiles, int max_rows, int pieces, RowsSpace ws) {
+    kv_rows_kernel(AttnParams p, int tiles, int max_rows, int pieces, bool together, RowsSpace ws) {
   using F = RowsCfg<D, NB>;
   using C = CellT<D>;
   constexpr int KM = D / 16;            // K-side matrix steps
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     b = reinterpret_cast<volatile int*>(sm + W + 1)[0];
   } else {
     const int item = blockIdx.x / pieces;
-    if (pieces > 1 && threadIdx.x == 0) ws.desc[blockIdx.x].joins = 0;
+    if (pieces > 1 && !together && threadIdx.x == 0) ws.desc[blockIdx.x].joins = 0;
     bt = item % tiles * p.pool.Hkv + (item / tiles) % p.pool.Hkv;
     b = item / tiles / p.pool.Hkv;
   }
@@ -293,9 +296,9 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     run1 = static_cast<int>(min(static_cast<int64_t>(rw.runs), run0 + (end - at)));
   } else if (pieces > 1) {
     const int share = max((rw.runs + pieces - 1) / pieces, W);
-    run0 = static_cast<int>(blockIdx.x) % pieces * share;
+    run0 = min(static_cast<int>(blockIdx.x) % pieces * share, rw.runs);
     run1 = min(run0 + share, rw.runs);
-    if (run0 >= rw.runs) return;
+    if (run0 >= rw.runs && !together) return;
   }
   const int tile = bt / p.pool.Hkv, kvh = bt - tile * p.pool.Hkv;
   const int len = rw.len, first = rw.first, n_new = rw.n_new, rows = rw.rows;
@@ -729,6 +732,39 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     }
     *reinterpret_cast<float2*>(part_o + r * F::LDO + d) = s;
   }
+  if (together) {
+    // every block joins its part of the rows from all blocks' shared memory, in their order
+    cluster_sync_all();
+    const uint32_t n = static_cast<uint32_t>(pieces);
+    for (int i = threadIdx.x + 32 * W * cta_rank(); i < F::R * (D / 2); i += 32 * W * n) {
+      const int r = i / (D / 2), d = 2 * (i % (D / 2));
+      if (!row_ok(r)) continue;
+      float2 ml[kCluster], u[kCluster];
+      float m = -INFINITY;
+#pragma unroll
+      for (uint32_t c = 0; c < kCluster; ++c) {
+        if (c >= n) break;
+        ml[c] = ld_cluster2(map_rank(sb + F::JOIN + 8 * r, c));
+        u[c] = ld_cluster2(map_rank(sb + 4 * (r * F::LDO + d), c));
+        m = fmaxf(m, ml[c].x);
+      }
+      float l = 0.f;
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t c = 0; c < kCluster; ++c) {
+        if (c >= n) break;
+        const float w = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - m);
+        l += ml[c].y * w;                                  // 0, or NaN where a key was NaN
+        o.x = __fmaf_rn(u[c].x, w, o.x);
+        o.y = __fmaf_rn(u[c].y, w, o.y);
+      }
+      const int tok = (row0 + r) / p.G;
+      const int64_t orow = static_cast<int64_t>(first + tok) * p.Hq + kvh * p.G + (row0 + r) - tok * p.G;
+      store_row(p, orow, D, d, o, m, l);
+    }
+    cluster_sync_all();                                    // the others have read this block's
+    return;
+  }
   __syncthreads();
   const bool whole = run0 == 0 && run1 == rw.runs;
   const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg > 0 ? 1 : 0);
@@ -857,6 +893,7 @@ struct RowsPlan {
   int64_t tiles;
   int64_t blocks;
   int pieces;          // blocks of an item, 0: the line of runs is cut evenly
+  bool together;       // an item's blocks are a cluster
 };
 template <int D, int NB>
 RowsPlan plan_rows(const AttnParams& p, int max_rows) {
@@ -870,25 +907,33 @@ RowsPlan plan_rows(const AttnParams& p, int max_rows) {
   // then whole items, if the requests are as long as each other (there is one), a share is at
   // most 16 runs a warp, or the blocks are so many that a long item is a small part of the
   // whole. No block then handles two items, which costs it a second round of latencies: one
-  // request of 2049 tokens and 32 heads takes 10.8 us against 15.7 on the even line, 33 of up to
+  // request of 2049 tokens and 32 heads took 10.8 us against 15.7 on the even line, 33 of up to
   // 4001 tokens 23.3 against 28.3, 64 of up to 8192 82.7 against 87.4. The even line else: it
   // does not depend on how the lengths, which the host does not know, are spread.
   int64_t pieces = items <= room ? room / items : 2 * items <= 5 * room ? 2 : 1;
   const int64_t useful = ceil_div(runs, W);
   if (pieces > useful) pieces = useful;
   if (p.n_req == 1 || ceil_div(runs, pieces) <= 16 * W || items >= 8 * room) {
+    // Up to eight blocks join their shares through distributed shared memory, without a second
+    // kernel and the workspace; more than eight are made eight where that leaves a warp no more
+    // than two runs. 10 requests of 2417 tokens, 4 x 7 heads: 12.4 -> 11.2 us, 33 of up to 4001
+    // with 5 drafted tokens 24.1 -> 21.2, one of 4096, 8 heads 10.2 -> 9.4, of 2049, 32 heads 10.6 ->
+    // 10.5 (and one launch less for the host); one of 8192, 32 heads (four runs) 15.8 -> 16.7.
+    if (pieces > kCluster && ceil_div(runs, kCluster) <= 2 * W) pieces = kCluster;
+    r.together = pieces > 1 && pieces <= kCluster;
     r.pieces = static_cast<int>(pieces);
     r.blocks = items * pieces;
     return r;
   }
   const int64_t parts = ceil_div(items * runs, W);
+  r.together = false;
   r.pieces = 0;
   r.blocks = parts < room ? parts : room;
   return r;
 }
 template <int D, int NB>
 size_t space_of(const RowsPlan& r, void* base, RowsSpace* ws) {
-  if (r.pieces == 1) return 0;
+  if (r.pieces == 1 || r.together) return 0;
   constexpr int R = 8 * NB;
   const size_t o = static_cast<size_t>(r.blocks) * 2 * R * D * 4, ml = static_cast<size_t>(r.blocks) * 2 * R * 8;
   if (ws) {
@@ -917,8 +962,14 @@ omq_status launch_rows(const AttnParams& p, int max_rows, void* space, cudaStrea
   const RowsPlan r = plan_rows<D, NB>(p, max_rows);
   RowsSpace ws = {};
   space_of<D, NB>(r, space, &ws);
-  launch_k(kv_rows_kernel<D, NB>, dim3(static_cast<unsigned>(r.blocks)), 32 * W, F::SMEM, st, p,
-           static_cast<int>(r.tiles), max_rows, r.pieces, ws);
+  const dim3 grid(static_cast<unsigned>(r.blocks));
+  if (r.together) {
+    launch_cl(kv_rows_kernel<D, NB>, grid, 32 * W, F::SMEM, r.pieces, st, p, static_cast<int>(r.tiles),
+              max_rows, r.pieces, true, ws);
+    return launch_status();
+  }
+  launch_k(kv_rows_kernel<D, NB>, grid, 32 * W, F::SMEM, st, p, static_cast<int>(r.tiles), max_rows,
+           r.pieces, false, ws);
   const omq_status s = launch_status();
   if (s != OMQ_OK || r.pieces == 1) return s;
   const int64_t most = static_cast<int64_t>(p.max_q) * p.G;

@@ -449,3 +449,21 @@ def test_many_weights_far_below_the_largest(omq, cuda_device, new, G, D, dt):
     assert np.all(np.abs(out[0, 0].double().cpu().numpy() - o) <= tol)
     if new * G <= 64:
         assert np.median(share / tol) > 1.3               # the bound tells the share from nothing
+
+
+@pytest.mark.parametrize("n_req,Hkv,G,new,D", [(1, 32, 1, 1, 128), (9, 8, 2, 1, 64), (20, 3, 4, 2, 128), (12, 8, 3, 5, 64),
+                                               (50, 4, 1, 1, 128), (3, 1, 8, 7, 128)])
+def test_shares_joined_by_their_blocks(omq, cuda_device, n_req, Hkv, G, new, D):
+    """Two to eight blocks an item; requests far shorter than the table, whose later shares are
+    empty, of one token, without any, or without a query."""
+    rng = np.random.default_rng(n_req)
+    lens = rng.integers(1, 700, n_req)
+    lens[0] = 1500
+    lens[1::4] = rng.integers(0, 3, len(lens[1::4]))
+    new = np.full(n_req, new)
+    new[2::5] = 0
+    s = Setup(cuda_device, lens.tolist(), new.tolist(), Hkv, G, D, 16, "f16", seed=79)
+    for causal in (True, False):
+        out, lse = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
+        omq.sync_check()
+        s.check(out, lse, causal, rows=3)
