@@ -660,8 +660,8 @@ typedef struct {
   const int32_t* table;        /* [n_req, width] */
   int64_t width;
   const int32_t* lens;         /* [n_req], the new tokens included */
-  const int32_t* cu;           /* [n_req + 1] */
-  int64_t max_q;               /* most rows of a request */
+  const int32_t* cu;           /* [n_req + 1], not decreasing, at most T */
+  int64_t max_q;               /* most rows of a request (further ones are not computed) */
   float scale;
   int causal;
   void* out;

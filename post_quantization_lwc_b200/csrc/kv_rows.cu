@@ -175,8 +175,8 @@ __device__ __forceinline__ ReqWork req_work(const AttnParams& p, int b, int max_
   ReqWork r;
   r.len = min(max(__ldg(p.lens + b), 0), p.width * p.pool.page);
   r.first = __ldg(p.cu + b);
-  r.n_new = min(max(__ldg(p.cu + b + 1) - r.first, 0), p.max_q);
-  r.rows = r.n_new * p.G;
+  r.n_new = max(__ldg(p.cu + b + 1) - r.first, 0);
+  r.rows = min(r.n_new, p.max_q) * p.G;
   r.tiles = r.rows > max_rows || r.first < 0 ? 0 : (r.rows + R - 1) / R;
   r.runs = max(1, (r.len + STEP - 1) / STEP);
   return r;

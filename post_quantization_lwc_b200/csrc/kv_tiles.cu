@@ -388,8 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (b < 0) return;                                           // the same for both CTAs
   const int len = min(max(p.lens[b], 0), p.width * p.pool.page);
   const int first = p.cu[b];
-  const int n_new = min(max(p.cu[b + 1] - first, 0), p.max_q);
-  const int rows = n_new * p.G;
+  const int n_new = max(p.cu[b + 1] - first, 0);
+  const int rows = min(n_new, p.max_q) * p.G;
   const int row0 = tile * ROWS;
 
   auto row_vis = [&](int r) {

@@ -467,3 +467,17 @@ def test_shares_joined_by_their_blocks(omq, cuda_device, n_req, Hkv, G, new, D):
         out, lse = omq.kv_attn(*s.args, s.max_q, causal=causal, lse=True)
         omq.sync_check()
         s.check(out, lse, causal, rows=3)
+
+
+@pytest.mark.parametrize("new,cut,G", [(7, 3, 2), (300, 140, 2), (40, 33, 4)])
+def test_rows_below_max_q_do_not_depend_on_it(omq, cuda_device, new, cut, G):
+    """Rows that a smaller max_q leaves in see the keys they see without it."""
+    s = Setup(cuda_device, [400, 310], [new, 2], 1, G, 64, 16, "f16", seed=83)
+    out = torch.zeros_like(s.args[0])
+    omq.kv_attn(*s.args, cut, out=out)
+    omq.sync_check()
+    s.new = np.array([cut, 2])                              # the rows to look at, and their keys
+    s.lens = np.array([400 - new + cut, 310])
+    s.kv = [[tuple(x[:n] for x in w) for w in r] for r, n in zip(s.kv, s.lens)]
+    s.check(out, rows=9)
+
