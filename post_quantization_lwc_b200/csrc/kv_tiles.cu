@@ -29,15 +29,15 @@
 //   8, 9      expand K; 10, 11 expand V
 //   12        MMA issue (leader CTA); TMEM allocation
 //   13        bulk copies of the raw cells
-// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 515 us (1.07 PFLOP/s), three chunks of up
-// to 1000 behind contexts of up to 16411 537 us (0.96); 32 heads, 2048 tokens 65 us (0.53: 4 to 16
-// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3600 cycles against
+// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 510 us (1.08 PFLOP/s), three chunks of up
+// to 1000 behind contexts of up to 16411 527 us (0.97); 32 heads, 2048 tokens 65 us (0.53: 4 to 16
+// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3550 cycles against
 // 2048 of products and another 2048 of exponentials (256 rows x 128 keys a CTA, 16 a clock); the
 // two meet only partly, a row's chain being read S, maximum, exponentials, write P with no more
 // than two subtiles in 512 columns of tensor memory. Tensor cores 52% busy, exponential unit 53%.
 // (Steps of 64 keys with two places for each subtile's scores, so that the next are ready when
-// a row's weights are done, took 652 us for 537: the narrower products of Q and K pass at the
-// pace of the wide ones.)
+// a row's weights are done, took 571 us: eight waits and twelve commits a tile of keys in the
+// issuing warp.)
 // Every mbarrier wait is bounded; on expiry the error flag is raised, every role stops, copies
 // and MMAs in flight are drained and both CTAs meet before TMEM is released. Loads never
 // multicast.
@@ -131,24 +131,24 @@ constexpr uint32_t idesc(int m, int n, bool b_mn) {
 // operand never has a second chunk within an instruction).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLead = 1u << 16;
-// Issued by the one lane of a converged warp that `leader` marks, with warp-uniform operands.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
-                                       uint32_t id, uint32_t acc) {
+// Issued by one lane, with operands that are the same for the whole warp.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
       "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
-      "r"(id), "r"(acc), "r"(kDescHi), "r"(leader));
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(id), "r"(acc), "r"(kDescHi));
 }
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
-                                       uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
       "mov.b64 db, {%2, %5};\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
-      "r"(id), "r"(acc), "r"(kDescHi), "r"(leader));
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(id), "r"(acc), "r"(kDescHi));
 }
 __device__ __forceinline__ uint32_t elect() {
   uint32_t r;
@@ -669,8 +669,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (warp == 12) {
     // ---------------------------------------------------------------- MMA issue
     // The whole warp walks the loop, so that addresses and descriptors stay warp-uniform; an
-    // elected lane issues. (One lane in a divergent branch spent 110 cycles an instruction on
-    // them beside four softmax warps of its scheduler, 3600 a tile of keys.)
+    // elected lane issues each group in a branch of its own: 21 to 26 cycles an instruction.
+    // (With the loop inside one lane's branch it was 110 beside four softmax warps of its
+    // scheduler, 3600 a tile of keys; with every instruction predicated 66, chunks of 1000 behind
+    // 16411 538 us for 527.)
     if (rank == 0 && nt > 0) {
       constexpr uint32_t id_qk = idesc(256, KT, false), id_pv = idesc(256, 128, true);
       const uint32_t leader = elect();
@@ -683,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int j = -1; j < nt; ++j) {
         // both operands' stages first: the waits between a subtile's weights and its next scores
-        // are on its critical path (chunks of 1000 behind 16411: 552 -> 537 us)
+        // are on its critical path (chunks of 1000 behind 16411: 552 -> 538 us)
         if (j >= 0) ok = wait_for(sb + F::VF + 8 * (j % NS), (j / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
         if (j + 1 < nt)
           ok = ok && wait_for(sb + F::KF + 8 * ((j + 1) % NS), ((j + 1) / NS) & 1, abort_flag, DEV_ERR_MMA_WAIT);
@@ -699,18 +701,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (!ok) break;
             tc_after();
             const uint32_t va = v_lo + st * (F::VST >> 4);
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk) {
-              if (kk == KT / 32) {                         // the weights' second half
-                ok = __all_sync(0xffffffffu, wait_for(sb + F::PG + 8 * s, j & 1, abort_flag, DEV_ERR_MMA_WAIT));
-                if (!ok) break;
-                tc_after();
-              }
-              mma_ts(leader, 256 + 128 * s, 128 * s + 8 * kk, va + ((kk * 2048) >> 4), id_pv,
-                     (j | kk) != 0);
-            }
-            if (!ok) break;
             if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < KT / 32; ++kk)
+                mma_ts(256 + 128 * s, 128 * s + 8 * kk, va + ((kk * 2048) >> 4), id_pv, (j | kk) != 0);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, wait_for(sb + F::PG + 8 * s, j & 1, abort_flag, DEV_ERR_MMA_WAIT));
+            if (!ok) break;
+            tc_after();                                    // the weights' second half
+            if (leader) {
+#pragma unroll
+              for (int kk = KT / 32; kk < KT / 16; ++kk)
+                mma_ts(256 + 128 * s, 128 * s + 8 * kk, va + ((kk * 2048) >> 4), id_pv, 1);
               commit_pair(sb + F::OF + 8 * s);
               if (s == 1 || j >= nt1) commit_pair(sb + F::VE + 8 * st);
             }
@@ -725,11 +728,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               tc_after();
             }
             const uint32_t qa = q_lo + s * (F::QSUB >> 4), ka = k_lo + st * (F::KST >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(leader, 128 * s, qa + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                     ka + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_qk, kk != 0);
             if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(128 * s, qa + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                     ka + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_qk, kk != 0);
               commit_pair(sb + F::SF + 8 * s);
               if (s == 1 || jn >= nt1) commit_pair(sb + F::KE + 8 * st);
             }
