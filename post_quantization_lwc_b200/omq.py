@@ -535,7 +535,8 @@ def kv_plan(lens, new_tokens, table, free_pages, n_free, page, capacity, in_plac
                    after + 4 * B if own else n_free.data_ptr(), at, maps, maps + 4 * capacity,
                    maps + 8 * capacity, capacity)
     _on(dev, _lib.omq_kv_plan, a)
-    cu, slots, positions, requests, l, f = buf.split_with_sizes(
+    # (the unsafe split keeps no record of views, which integers have no use for)
+    cu, slots, positions, requests, l, f = buf.unsafe_split_with_sizes(
         (B + 1, capacity, capacity, capacity, own * B, own))
     return {"lens": l if own else lens, "n_free": f if own else n_free, "cu": cu, "slots": slots,
             "positions": positions, "requests": requests}
