@@ -136,3 +136,33 @@ def test_captured_decoding_steps(omq, cuda_device):
         assert torch.equal(out_a[:n], out_b[:n]), i
         assert torch.equal(a.cache.table, b.cache.table)
     omq.sync_check()
+
+
+def test_a_whole_step_on_a_side_stream(omq, cuda_device):
+    """plan, append, read and attend with stream=, and the rotary table made there, give what
+    they give on the current stream; a stream of no device that fits is refused."""
+    side, got = torch.cuda.Stream(), []
+    for stream in (None, side):
+        s = Server(omq, cuda_device, 3, 60, 2, 2, 64, 16, 16)
+        rope = omq.rope_table(512, 64, device="cuda", stream=stream)
+        x = [s.qkv(40).to(cuda_device).half() for _ in range(2)]
+        torch.cuda.synchronize()
+        for new, rows in zip(([20, 0, 17], [1, 3, 1]), x):
+            new = torch.tensor(new, dtype=torch.int32, device=cuda_device)
+            torch.cuda.synchronize()
+            step = s.cache.plan(new, rows.shape[0], stream=stream)
+            q, k, v = s.split(rows)
+            qt = torch.zeros(40, 4, 64, dtype=torch.float16, device=cuda_device)
+            torch.cuda.synchronize()
+            s.cache.append(step, k, v, q, q_out=qt, stream=stream)
+            out = torch.zeros_like(qt)
+            torch.cuda.synchronize()
+            s.cache.attend(step, qt, 20, out=out, stream=stream)
+            kk, vv = omq.kv_read(s.cache.pool, step["slots"], stream=stream)
+            torch.cuda.synchronize()
+            got.append([rope, step["slots"].clone(), qt, out, kk, vv, s.cache.lens.clone()])
+    omq.sync_check()
+    for a, b in zip(got[:2], got[2:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    with pytest.raises(ValueError):
+        omq.rope_table(8, 64, device="cpu", stream=side)
