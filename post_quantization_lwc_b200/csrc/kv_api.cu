@@ -69,29 +69,56 @@ omq_status check_attn(const omq_kv_attn_args* a) {
   return OMQ_OK;
 }
 
-// Query rows per kv head up to which a request goes to the row kernel, whose time grows with the
-// rows (it expands the codes again for every 16), while the tile kernel's does not up to 512.
-// Row / tile kernel, us, at 64 rows and at 128: 8 requests of 4096 tokens and 8 kv heads 48 / 70
-// and 118 / 71; 32 of 2048 107 / 149 and 195 / 154; one of 65536 84 / 126 and 166 / 127; one of
-// 4096 tokens and 32 kv heads 33 / 44 and 48 / 45; 8 kv heads of 64 values 15 / 19 and 18 / 20.
-constexpr int kFew = 64;
-
-int64_t most_rows(const omq_kv_attn_args* a) { return a->max_q * (a->Hq / a->pool.Hkv); }
-bool uses_rows(const omq_kv_attn_args* a) { return most_rows(a) <= kFew || a->n_req > 1; }
-bool uses_tiles(const omq_kv_attn_args* a) { return most_rows(a) > kFew; }
-// Where both kernels run, each takes the requests of its kind, by the lengths on the device.
-int tiles_min(const omq_kv_attn_args* a) { return uses_rows(a) ? kFew + 1 : 0; }
 kv::AttnParams attn_params(const omq_kv_attn_args* a) {
   return kv::AttnParams{view(a->pool), static_cast<int>(a->n_req), a->T, static_cast<int>(a->Hq),
                         static_cast<int>(a->Hq / a->pool.Hkv), a->q, a->q_ld, a->dt, a->table,
                         static_cast<int>(a->width), a->lens, a->cu, static_cast<int>(a->max_q),
                         a->scale, a->causal ? 1 : 0, a->out, a->out_dt, a->lse};
 }
-// The kernels run one after the other and share the workspace.
-size_t attn_space(const omq_kv_attn_args* a, const kv::AttnParams& p) {
-  const size_t r = uses_rows(a) ? kv::attn_rows_space(p, a->pool.D, kFew) : 0;
-  const size_t t = uses_tiles(a) ? kv::attn_tiles_space(p, a->pool.D, tiles_min(a)) : 0;
-  return r > t ? r : t;
+// Query rows per kv head up to which a request goes to the row kernel, whose time grows with the
+// rows (it expands the codes again for every 16), while the tile kernel's does not up to 512.
+// 64 wherever the contexts are long. Row / tile kernel, us, at 64 rows and at 128: 8 requests of
+// 4096 tokens and 8 kv heads 48 / 70 and 118 / 71; 32 of 2048 107 / 149 and 195 / 154; one of 65536
+// 84 / 126 and 166 / 127; one of 4096 tokens and 32 kv heads 33 / 44 and 48 / 45; 8 kv heads of 64
+// values 15 / 19 and 18 / 20. Under short contexts the tile kernel's fixed 8 us an item weigh more
+// than the repeated codes, and all requests of up to 512 rows go to the row kernel where its
+// estimate is below the other's: 10 us to begin and end and, while all blocks are resident, 3 for
+// a run of 64 tokens a warp, else (half with D = 64) 5 a run and 1 a wave of blocks. One prompt of
+// 512 tokens, 8 heads 20.4 -> 13.9 us; 39 of up to 124 tokens, 8 heads of 64 the same (42). Float16
+// results may take half as long again there: its exact operands keep their last bit (error 2.2e-4
+// of the result against 3.4e-4, where rounding the result alone gives 2.1e-4).
+constexpr int kFew = 64, kFewShort = 512;
+
+int64_t most_rows(const omq_kv_attn_args* a) { return a->max_q * (a->Hq / a->pool.Hkv); }
+int few_rows(const omq_kv_attn_args* a, const kv::AttnParams& p) {
+  const int64_t most = most_rows(a);
+  if (most <= kFew || most > kFewShort) return kFew;
+  const int64_t items = ceil_div(most, 16) * a->pool.Hkv * a->n_req;
+  const int64_t runs = ceil_div(a->width * a->pool.page, 64), room = 2 * num_sms();
+  const int64_t wave = (5 * ceil_div(runs, 4) + 1) * a->pool.D / 128;
+  const int64_t rows_us = 10 + (items <= room ? 3 * ceil_div(items * runs, 4 * room)
+                                              : ceil_div(items, room) * wave);
+  const int64_t tiles_us = kv::attn_tiles_us(p, a->n_req == 1 ? 0 : kFew + 1);
+  return (a->out_dt == OMQ_F16 ? 2 * rows_us <= 3 * tiles_us : rows_us <= tiles_us) ? kFewShort : kFew;
+}
+// What a call launches: the tile kernel for the requests of at least tiles_min rows (if any is),
+// the row kernel for those of at most `few`, by the lengths on the device. They run one after
+// the other and share the workspace.
+struct AttnRoute {
+  int few, tiles_min;
+  bool rows, tiles;
+  size_t space;
+};
+AttnRoute attn_route(const omq_kv_attn_args* a, const kv::AttnParams& p) {
+  AttnRoute r;
+  r.few = few_rows(a, p);
+  r.tiles = most_rows(a) > r.few;
+  r.rows = !r.tiles || a->n_req > 1;
+  r.tiles_min = r.rows ? r.few + 1 : 0;
+  const size_t rows = r.rows ? kv::attn_rows_space(p, a->pool.D, r.few) : 0;
+  const size_t tiles = r.tiles ? kv::attn_tiles_space(p, a->pool.D, r.tiles_min) : 0;
+  r.space = rows > tiles ? rows : tiles;
+  return r;
 }
 
 }  // namespace
@@ -197,7 +224,7 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
 size_t omq_kv_attn_workspace_bytes(const omq_kv_attn_args* a) {
   if (check_attn(a) != OMQ_OK) return 0;
   const kv::AttnParams p = attn_params(a);
-  return attn_space(a, p);
+  return attn_route(a, p).space;
 }
 
 omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_bytes,
@@ -205,11 +232,11 @@ omq_status omq_kv_attn(const omq_kv_attn_args* a, void* workspace, size_t ws_byt
   KV_TRY(check_attn(a));
   const kv::AttnParams p = attn_params(a);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const size_t need = attn_space(a, p);
-  if (need && (!workspace || ws_bytes < need)) return OMQ_ERR_WORKSPACE;
+  const AttnRoute r = attn_route(a, p);
+  if (r.space && (!workspace || ws_bytes < r.space)) return OMQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return OMQ_ERR_ALIGN;
-  if (uses_tiles(a)) KV_TRY(kv::launch_attn_tiles(p, a->pool.D, tiles_min(a), workspace, st));
-  return uses_rows(a) ? kv::launch_attn_rows(p, a->pool.D, kFew, workspace, st) : OMQ_OK;
+  if (r.tiles) KV_TRY(kv::launch_attn_tiles(p, a->pool.D, r.tiles_min, workspace, st));
+  return r.rows ? kv::launch_attn_rows(p, a->pool.D, r.few, workspace, st) : OMQ_OK;
 }
 
 }  // extern "C"

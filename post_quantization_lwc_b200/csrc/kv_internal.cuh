@@ -115,6 +115,7 @@ size_t attn_rows_space(const AttnParams& p, int64_t D, int max_rows);   // bytes
 // Attention of the requests with at least min_rows query rows per kv head, 512 rows a CTA pair.
 omq_status launch_attn_tiles(const AttnParams& p, int64_t D, int min_rows, void* space,
                              cudaStream_t st);
+int64_t attn_tiles_us(const AttnParams& p, int min_rows);   // estimate for full tables
 size_t attn_tiles_space(const AttnParams& p, int64_t D, int min_rows);
 
 // Per translation unit with barrier waits: read and clear its error flag, set its wait limit

@@ -934,6 +934,7 @@ struct TilesPlan {
   int64_t list;        // row tiles of all requests, at most
   int64_t items;       // the same of all kv heads
   int pieces;          // pairs that share an item's keys
+  int64_t us;          // estimated time of requests of equal lengths
 };
 TilesPlan plan_tiles(const AttnParams& p, int min_rows) {
   TilesPlan r;
@@ -963,6 +964,7 @@ TilesPlan plan_tiles(const AttnParams& p, int min_rows) {
     if (n == 1 || us < best) {
       best = us;
       r.pieces = static_cast<int>(n);
+      r.us = equal + (n > 1 ? 6 : 0);
     }
   }
   return r;
@@ -1019,6 +1021,8 @@ omq_status launch_tiles(const AttnParams& p, int min_rows, void* space, cudaStre
 }
 
 }  // namespace
+
+int64_t attn_tiles_us(const AttnParams& p, int min_rows) { return plan_tiles(p, min_rows).us; }
 
 size_t attn_tiles_space(const AttnParams& p, int64_t D, int min_rows) {
   const TilesPlan r = plan_tiles(p, min_rows);
