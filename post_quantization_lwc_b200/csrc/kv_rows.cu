@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
           mt[i].z = bad ? 0.f : lg2(vh);
           mt[i].w = there ? static_cast<float>(lds_i(a + 192)) : 0.f;
         }
+        __syncwarp();                    // a lane's entries lie over steps that others read
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int en = lane + 32 * i;
