@@ -648,18 +648,24 @@ class KVCache:
     table, the lengths and the stack of free pages. One serving step is ``plan`` (pages, slots
     and positions of the step's new tokens), ``append`` (their k and v, and q made ready) and
     ``attend``; all of it may be captured in a CUDA graph, with ``new_tokens`` and the
-    activations in fixed buffers."""
+    activations in fixed buffers. A request holds up to ``max_len`` tokens, rounded up to whole
+    pages; the rotary table has that many positions, or ``n_pos`` if it is more."""
 
     def __init__(self, n_req, n_pages, Hkv, D, page=64, max_len=4096, n_pos=None, base=10000.0,
                  device="cuda"):
         i32 = dict(dtype=torch.int32, device=device)
         self.pool = kv_pool(n_pages, Hkv, D, page, device)
         self.page = page
-        self.table = torch.full((n_req, -(-max_len // page)), -1, **i32)
+        width = -(-max_len // page)
+        # the plan grants every position of the table, and append skips those it cannot rotate
+        n_pos = n_pos or width * page
+        if n_pos < width * page:
+            raise ValueError(f"n_pos is at least max_len in whole pages, here {width * page}")
+        self.table = torch.full((n_req, width), -1, **i32)
         self.lens = torch.zeros(n_req, **i32)
         self.free_pages = torch.arange(n_pages - 1, -1, -1, **i32)     # page 0 on top
         self.n_free = torch.full((1,), n_pages, **i32)
-        self.rope = rope_table(n_pos or max_len, D, base, device)
+        self.rope = rope_table(n_pos, D, base, device)
 
     def plan(self, new_tokens, capacity, stream=None):
         """omq_kv_plan in place: dict(lens, n_free, cu, slots, positions, requests)."""
