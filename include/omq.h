@@ -643,9 +643,10 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * rounded to float16 (what is below 2^-39, with many rows 2^-31, of the row's largest is lost),
  * q exactly unless an element is 2^-28 of the largest of the rows it is processed with. For a
  * request of more than 64 query rows per kv head (rows = tokens x Hq / Hkv), k and v themselves
- * may be float16 operands, rounded once (so |k scale log2 e| and |v| below 65504, and |v| to no
- * finer than 2^-25): always for more than 512 rows, below by the call's sizes and types. Results are bitwise reproducible on one device. out and lse overlap nothing
- * that is read (out over q: OMQ_ERR_UNSUPPORTED).
+ * may be float16 operands (so |k scale log2 e| and |v| below 65504, and each to within 2^-11 of
+ * it and 2^-25): always for more than 512 rows, below by the call's sizes and types. Results are
+ * bitwise reproducible on one device. out and lse overlap nothing that is read (out over q:
+ * OMQ_ERR_UNSUPPORTED).
  * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL), 16-byte aligned, from
  * a query under the device of the call; its contents are nothing before and after. Calls (and
  * graphs) that may run at the same time need one each.

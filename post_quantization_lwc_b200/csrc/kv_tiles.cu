@@ -3,7 +3,7 @@
 //
 //   x_ij = q_i . k'_j,  k'_j = scale log2(e) (c_j - z_j) hk_j;   w_ij = 2^(x_ij - m_i + 7)
 //   o_i  = sum_j w_ij v_j / sum_j w_ij,  v_j = (c_j - z_j) hv_j
-// k', v and w are float16 operands, each rounded once (relative 2^-12), as in the calibrated block's
+// k', v and w are float16 operands, each rounded once (by at most 2^-11 of it), as in the calibrated block's
 // own attention; statistics, sums and accumulators are float32. (Keeping the steps outside the
 // products, as kv_rows.cu does, costs three broadcast shared loads per score here: 393 KB a
 // tile of keys against 128 B a clock, more than the products' time.) The reference m_i follows
@@ -229,9 +229,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// What expand() needs of a row: the step in two float16 parts, and 1024 + z, 64 + z (twice each).
-// |z| <= 960 is exact in them; the few rows beyond (all values 60 times further from zero than
-// they spread) take the slow path.
+// What expand() needs of a row: the step as two float16, hi + lo 2^-11 (lo as large as hi's last
+// bit allows, so that it keeps its own bits down to a step of 2^-14), and 1024 + z, 64 + z (twice
+// each). |z| <= 960 is exact in them. The rows beyond (all values 60 times further from zero than
+// they spread) and those of smaller steps take the slow path. (With lo as a plain float16 a step
+// below 2^-9 was off by up to 2^-25, times c - z: a value row of 0.01 +- 1e-4 by 2.6e-3 of it.
+// Chunks of 1000 behind 16411 take 527 us for 523 with the product more; where every step of K
+// is around 2^-14, so that warps take both paths, 880.)
+constexpr float kSmallStep = 6.103515625e-05f;             // 2^-14
 struct RowSteps {
   uint32_t hi, lo, z10, z6;
   float h, z;
@@ -242,18 +247,19 @@ __device__ __forceinline__ RowSteps row_steps(float h, float z) {
   const float hi = __half2float(__float2half_rn(h));
   r.hi = pack_h2(hi, hi);
   // (an infinite or NaN step has no remainder)
-  const float lo = fabsf(hi) < INFINITY ? h - hi : 0.f;
+  const float lo = fabsf(hi) < INFINITY ? (h - hi) * 2048.f : 0.f;
   r.lo = pack_h2(lo, lo);
   r.z10 = pack_h2(-1024.f - z, -1024.f - z);
   r.z6 = pack_h2(-64.f - z, -64.f - z);
   r.h = h;
   r.z = z;
-  r.slow = fabsf(z) > 960.f;
+  r.slow = fabsf(z) > 960.f || (h != 0.f && fabsf(h) < kSmallStep);
   return r;
 }
 // (c - z) h of a word's eight codes in the order 0 4 1 5 2 6 3 7: a code placed in the mantissa
 // of 1024 (or, in the next nibble, as 16 c) gives c - z exactly, and with the step in two parts
-// the product is rounded once but for 2^-22 of it.
+// the product is rounded once but for 2^-20 of it and, where the second part's product is a
+// subnormal, 2^-25.
 __device__ __forceinline__ void expand(uint32_t w, const RowSteps& r, uint32_t addr) {
   uint32_t o[4];
   const uint32_t w8 = w >> 8;
@@ -262,8 +268,13 @@ __device__ __forceinline__ void expand(uint32_t w, const RowSteps& r, uint32_t a
                          hadd2((w8 & 0x000F000Fu) | 0x64006400u, r.z10),
                          hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, r.z6)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = hfma2(d[i], r.hi, hmul2(d[i], r.lo));
+  for (int i = 0; i < 4; ++i) o[i] = hfma2(d[i], r.hi, hmul2(hmul2(d[i], r.lo), 0x10001000u));
   sts4(addr, o[0], o[1], o[2], o[3]);
+}
+// The same in float32, rounded once. (A code is read as a number from the mantissa of 2^23: the
+// conversion instruction runs on the exponentials' unit.)
+__device__ __forceinline__ float slow_value(uint32_t c, float h, float z) {
+  return ((__uint_as_float(c | 0x4B000000u) - 8388608.f) - z) * h;
 }
 __device__ __noinline__ void expand_slow(uint4 w, float h, float z, uint32_t base, int j0, int sw) {
 #pragma unroll 1
@@ -272,8 +283,7 @@ __device__ __noinline__ void expand_slow(uint4 w, float h, float z, uint32_t bas
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      o[i] = pack_h2((static_cast<float>((u >> (4 * i)) & 15u) - z) * h,
-                     (static_cast<float>((u >> (4 * i + 16)) & 15u) - z) * h);
+      o[i] = pack_h2(slow_value((u >> (4 * i)) & 15u, h, z), slow_value((u >> (4 * i + 16)) & 15u, h, z));
     sts4(base + (((j0 + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
   }
 }

@@ -25,8 +25,8 @@ def tile_kernel(s, b):
 def attend_tiles(q, k, v, scale, out_half_step):
     """One query row in binary64 against the keys it sees, k and v [N, D]. Returns (o, lse, bound
     of |o|'s error, bound of lse's error) of the tile kernel:
-      operands  k' = scale log2(e) k and v, rounded to float16: 2^-11 and, for the two parts of
-                their step, 2^-15 of their size, and 2^-25; q, float16 or within its range: 2^-25
+      operands  k' = scale log2(e) k and v, rounded to float16: 2^-11 of their size (and 2^-20 for
+                the two parts of their step), and 2^-25; q, float16 or within its range: 2^-25
       score     D products of the rounded operands summed in float32, the matrix unit's partial
                 sums to 2^-22; 2^x to 2^-22 of |x| + 1 in the exponent: e, in binary digits
       weights   every p by 2 e ln 2 (numerator and sum); as float16, at least 2^7 for the largest:
@@ -37,7 +37,7 @@ def attend_tiles(q, k, v, scale, out_half_step):
     if n == 0:
         return np.zeros(d), -np.inf, np.zeros(d), 0.0
     log2e = 1.4426950408889634
-    part = 2.0 ** -11 + 2.0 ** -15
+    part = 2.0 ** -11 + 2.0 ** -20
     x = k @ q * scale
     top = x.max()
     p = np.exp(x - top)
