@@ -597,10 +597,12 @@ omq_status omq_kv_plan(const omq_kv_plan_args* args, omq_stream_t stream);
  *   k~ = RoPE(k) s_a, v~ = (v - delta_o) / s_o, q~ = RoPE(q) / s_a
  *   h = max((max - min) / 15, 1e-8), z = -round(min / h), c = clamp(round(x / h) + z, 0, 15)
  *   q_out = q~ in q_dt, or for abits < 16 its fake-quant with 2^abits - 1 in place of 15
- * A row holding a NaN or an infinity, or whose range overflows, is stored with h = NaN and
- * reads back as NaN; z is kept within +-2^30 (a constant row beyond 10.7 is cut there). RoPE takes pairs (i, i + D/2) and row positions[t] of the table; no
- * positions (or no table): no rotation. s_a, s_o, delta_o [Hkv, D] or NULL (no transform);
- * query head j shares those of kv head j / (Hq / Hkv).
+ * A row holding a NaN or an infinity, or whose range or min / h overflows, is stored with
+ * h = NaN and reads back as NaN. A row whose |z| is above 2^30 (a constant one beyond 10.7) is
+ * stored as c = 0, z = -1 or 1, h = |z h|, which is the same value. RoPE takes pairs
+ * (i, i + D/2) and row positions[t] of the table; no positions (or no table): no rotation.
+ * s_a, s_o, delta_o [Hkv, D] or NULL (no transform); query head j shares those of kv head
+ * j / (Hq / Hkv).
  * q, k, v: [T, Hq or Hkv, D] in dt, a token's heads back to back, tokens q_ld / k_ld / v_ld
  * elements apart (slices of one fused product are fine; rows 16-byte aligned). q may be NULL.
  * q_out [T, Hq, D] dense, overlapping none of q, k, v (OMQ_ERR_UNSUPPORTED). A token whose slot is outside the pool (-1 in particular) or whose

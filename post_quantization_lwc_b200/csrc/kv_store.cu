@@ -230,13 +230,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
   if (quant) {
     const float Q = which == 0 ? p.Qa : 15.f;
     GroupQ g = group_params(1.f, 1.f, vmax, vmin, Q);
-    // a row that is not finite, or whose range is not, reads back as NaN throughout
-    if (bad || !(g.h < INFINITY)) {
+    // a row that is not finite, or whose range or quotients are not, reads back as NaN throughout
+    if (bad || !(g.h < INFINITY) || !(fabsf(g.z) < INFINITY)) {
       g.h = NAN;
       g.z = 0.f;
     }
     const float hinv = __frcp_rn(g.h);
-    const int zi = z_to_i32(g.z);
+    int zi = z_to_i32(g.z);
     const float umax = fmaxf(fabsf(vmax), fabsf(vmin)) * hinv;
     const float thr = umax < 2000.f ? 0.49999f - 2.384185791015625e-07f * umax : -1.f;
     float2 ta[E / 2], tb[E / 2];
@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
         wb |= static_cast<uint32_t>(b0 | b1 << 4) << (8 * k);
       }
     } else {
-      const float z = static_cast<float>(zi);
       auto code = [&](float x) {
         return fminf(fmaxf(__fadd_rn(round_quotient(x, g.h, hinv), g.z), 0.f), Q);
       };
@@ -277,12 +276,18 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
       for (int k = 0; k < E / 2; ++k) {
         const float a0 = code(a[k].x), a1 = code(a[k].y), b0 = code(b[k].x), b1 = code(b[k].y);
         if (which == 0) {
-          a[k] = make_float2(__fmul_rn(__fsub_rn(a0, z), g.h), __fmul_rn(__fsub_rn(a1, z), g.h));
-          b[k] = make_float2(__fmul_rn(__fsub_rn(b0, z), g.h), __fmul_rn(__fsub_rn(b1, z), g.h));
+          a[k] = make_float2(__fmul_rn(__fsub_rn(a0, g.z), g.h), __fmul_rn(__fsub_rn(a1, g.z), g.h));
+          b[k] = make_float2(__fmul_rn(__fsub_rn(b0, g.z), g.h), __fmul_rn(__fsub_rn(b1, g.z), g.h));
         } else {
           wa |= (small_uint(a0) | small_uint(a1) << 4) << (8 * k);
           wb |= (small_uint(b0) | small_uint(b1) << 4) << (8 * k);
         }
+      }
+      // A zero point beyond the stored integer's range has a step of 1e-8, so a row whose values
+      // are all one float32: codes 0, and the same value (0 - z) h with z = -1 or 1.
+      if (fabsf(g.z) > static_cast<float>(Z_LIMIT)) {
+        zi = g.z < 0.f ? -1 : 1;
+        g.h = fabsf(__fmul_rn(g.z, g.h));
       }
     }
     if (which != 0) {
