@@ -637,10 +637,19 @@ def kv_attn(q, pool, table, lens, cu, max_q, scale=None, causal=True, out=None, 
                    lens.data_ptr(), cu.data_ptr(), max_q, D ** -0.5 if scale is None else scale,
                    1 if causal else 0, out.data_ptr(), _dt(out),
                    0 if ls is None else ls.data_ptr())
+    _attn(dev, a)
+    return (out, ls) if lse else out
+
+
+def _attn(dev, a):
+    """omq_kv_attn with a workspace for the call. Its size is asked for under the tensors' device,
+    whose number of SMs decides how the work is laid out."""
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev.index):
+            return _attn(dev, a)
     n = _lib.omq_kv_attn_workspace_bytes(a)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     _on(dev, _lib.omq_kv_attn, a, None if ws is None else ws.data_ptr(), n)
-    return (out, ls) if lse else out
 
 
 class KVCache:
