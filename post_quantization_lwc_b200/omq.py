@@ -498,7 +498,8 @@ def _rows(device, t, shape, D):
 def rope_table(n_pos, D, base=10000.0, device="cuda", stream=None) -> torch.Tensor:
     """omq_rope_table: float32 [2, n_pos, D/2], cos and sin of position * base^(-2i/D)."""
     if stream is not None:
-        with _with(stream, stream.device if device == "cuda" else torch.device(device)):
+        at = torch.device(device)
+        with _with(stream, stream.device if at == torch.device("cuda") else at):
             return rope_table(n_pos, D, base, stream.device)
     t = torch.empty(2, n_pos, D // 2, dtype=torch.float32, device=device)
     _on(t.device, _lib.omq_rope_table, n_pos, D, float(base), t.data_ptr())

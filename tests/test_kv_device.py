@@ -62,3 +62,19 @@ def test_workspace_is_sized_under_the_tensors_device(omq, monkeypatch, current, 
     out = omq.kv_attn(q, pool, ints(2, 2), ints(2), ints(3), 3, out=Tensor((3, 2, 128), torch.float16, dev))
     assert out.shape == q.shape and now == [current]
     assert seen == [("size", theirs), ("attn", theirs, 100 + theirs)]
+
+
+class Entered(Exception):
+    pass
+
+
+@pytest.mark.parametrize("device,theirs", [("cuda", 1), (torch.device("cuda"), 1), ("cuda:1", 1), (torch.device("cuda", 0), 0)])
+def test_rope_table_takes_the_stream_s_device(omq, monkeypatch, device, theirs):
+    """A device without a number is the stream's, however it is written."""
+    def stream_context(s):
+        raise Entered(s.device)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(Entered if theirs == 1 else ValueError):
+        omq.rope_table(8, 64, device=device, stream=stream)
