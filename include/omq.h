@@ -642,13 +642,14 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * q [T, Hq, D] F16 or BF16, tokens q_ld elements apart, rows 16-byte aligned; out [T, Hq, D]
  * dense, F16 or BF16; lse [T, Hq] float32 (natural log of the softmax's denominator) or NULL.
  * The codes are exact operands and sums, statistics and steps are float32; the weights are
- * rounded to float16 (what is below 2^-39, with many rows 2^-31, of the row's largest is lost),
- * q exactly unless an element is 2^-28 of the largest of the rows it is processed with. For a
- * request of more than 64 query rows per kv head (rows = tokens x Hq / Hkv), k and v themselves
- * may be float16 operands (so |k scale log2 e| and |v| below 65504, and each to within 2^-11 of
- * it and 2^-25): always for more than 512 rows, below by the call's sizes and types. Results are
- * bitwise reproducible on one device. out and lse overlap nothing that is read (out over q:
- * OMQ_ERR_UNSUPPORTED).
+ * rounded to float16 (what is below 2^-39, with many rows 2^-31, of the row's largest is lost).
+ * q counts to within 2^-35 of the largest element (below 2^115) of the 8 or 16 rows that are
+ * processed together; with many rows float16 exactly, bfloat16 to within 2^-25, or 2^-39 of the
+ * row's largest where that is below 2^-10 or from 2^15 on. For a request of more than 64 query
+ * rows per kv head (rows = tokens x Hq / Hkv), k and v themselves may be float16 operands (so
+ * |k scale log2 e| and |v| below 65504, and each to within 2^-11 of it and 2^-25): always for
+ * more than 512 rows, below by the call's sizes and types. Results are bitwise reproducible on
+ * one device. out and lse overlap nothing that is read (out over q: OMQ_ERR_UNSUPPORTED).
  * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL), 16-byte aligned, from
  * a query under the device of the call; its contents are nothing before and after. Calls (and
  * graphs) that may run at the same time need one each.

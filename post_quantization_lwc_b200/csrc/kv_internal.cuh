@@ -1,6 +1,6 @@
 // Internal declarations of the 4-bit paged key/value cache (kv_api.cu, kv_plan.cu, kv_store.cu,
-// kv_decode.cu): the pool's layout, launch helpers with clusters, and the shared-memory
-// barrier, bulk-copy and matrix-instruction wrappers of its kernels.
+// kv_rows.cu, kv_tiles.cu): the pool's layout, launch helpers with clusters, and the
+// shared-memory barrier, bulk-copy and matrix-instruction wrappers of its kernels.
 //
 // Pool: uint8 [n_pages, Hkv, page / 16, cell]. A cell holds 16 consecutive tokens of one kv
 // head, 16 D + 256 bytes back to back, so one bulk copy brings everything a kernel needs of

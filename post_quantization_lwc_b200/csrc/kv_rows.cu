@@ -1,5 +1,6 @@
 // Attention of a few query rows over the 4-bit paged cache (decoding, drafted tokens, chunks of
-// up to 64 rows per kv head), a tile of 8 or 16 rows at a time.
+// up to 64 rows per kv head and, under short contexts, up to 512), a tile of 8 or 16 rows at a
+// time.
 //
 // o = sum_j p_j v_j with p = softmax_j(scale q . k_j), k_j = (c - z) h and v_j alike. The codes
 // themselves are the matrix instructions' operands and the steps stay outside, in binary32:
@@ -8,10 +9,12 @@
 //   o             = (sum_j w_j cv_jd - sum_j w_j zv_j) / sum_j (w_j / hv_j)
 // so w_j = p_j hv_j up to the row's common factor lies in [0, 2^15] for any hv and its rounding to
 // float16 (the operand; the same rounded value weighs zv_j) is relative to the largest
-// contribution (zero points far from the codes: see kFarZ). A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
+// contribution (zero points far from the codes: see kFarZ); the denominator sums the weights as
+// they were, the largest exact in both. A code c < 16 is the float16 subnormal c 2^-24 as it stands, 16 c 2^-24 in the
 // second nibble of a 16-bit lane: one AND makes two operands, exact, and the powers of two go
-// into q (the odd nibbles' q times 1/16; the tile's q scaled by a power of two, so both input
-// types are exact but for values 2^-28 below the tile's largest) and into the result.
+// into q (the odd nibbles' q times 1/16; the tile's q scaled by a power of two, so float16 is
+// exact down to 2^-24 of the tile's largest, bfloat16 to 2^-27, and what is below to 2^-35 of it)
+// and into the result.
 //
 // The floor is the cache's bytes: D + 16 per token and kv head. The work is a line of runs of
 // 64 tokens, item after item (an item: request, tile of 8 NB rows, kv head), cut into equal parts,
@@ -906,8 +909,8 @@ RowsPlan plan_rows(const AttnParams& p, int max_rows) {
   const int64_t room = (NB == 1 ? 3 : 2) * static_cast<int64_t>(num_sms());
   // Equal shares of each item while all blocks are resident at once, two up to 2.5 times that,
   // then whole items, if the requests are as long as each other (there is one), a share is at
-  // most 16 runs a warp, or the blocks are so many that a long item is a small part of the
-  // whole. No block then handles two items, which costs it a second round of latencies: one
+  // most 16 runs a warp (the last case below lies on that limit), or the blocks are eight times
+  // those resident (a request far longer than the others then ends alone). No block then handles two items, which costs it a second round of latencies: one
   // request of 2049 tokens and 32 heads took 10.8 us against 15.7 on the even line, 33 of up to
   // 4001 tokens 23.3 against 28.3, 64 of up to 8192 82.7 against 87.4. The even line else: it
   // does not depend on how the lengths, which the host does not know, are spread.

@@ -3,8 +3,9 @@
 //
 //   x_ij = q_i . k'_j,  k'_j = scale log2(e) (c_j - z_j) hk_j;   w_ij = 2^(x_ij - m_i + 7)
 //   o_i  = sum_j w_ij v_j / sum_j w_ij,  v_j = (c_j - z_j) hv_j
-// k', v and w are float16 operands, each rounded once (by at most 2^-11 of it), as in the calibrated block's
-// own attention; statistics, sums and accumulators are float32. (Keeping the steps outside the
+// k', v and w are float16 operands, each rounded once (by at most 2^-11 of it), as in the
+// calibrated block's own attention; statistics, sums (of the weights before their rounding) and
+// accumulators are float32. (Keeping the steps outside the
 // products, as kv_rows.cu does, costs three broadcast shared loads per score here: 393 KB a
 // tile of keys against 128 B a clock, more than the products' time.) The reference m_i follows
 // the row's maximum only when that has grown by more than 2^8, so o is rescaled rarely; in
@@ -29,12 +30,13 @@
 //   8, 9      expand K; 10, 11 expand V
 //   12        MMA issue (leader CTA); TMEM allocation
 //   13        bulk copies of the raw cells
-// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 510 us (1.08 PFLOP/s), three chunks of up
-// to 1000 behind contexts of up to 16411 527 us (0.97); 32 heads, 2048 tokens 65 us (0.53: 4 to 16
-// tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3550 cycles against
+// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 505 us (1.09 PFLOP/s) in a burst at
+// 1965 MHz and 567 under load at the power limit (1762 MHz), three chunks of up to 1000 behind
+// contexts of up to 16411 527 us (0.97) and 558 (1867 MHz); 32 heads, 2048 tokens 65 us (0.53: 4 to
+// 16 tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3550 cycles against
 // 2048 of products and another 2048 of exponentials (256 rows x 128 keys a CTA, 16 a clock); the
 // two meet only partly, a row's chain being read S, maximum, exponentials, write P with no more
-// than two subtiles in 512 columns of tensor memory. Tensor cores 52% busy, exponential unit 53%.
+// than two subtiles in 512 columns of tensor memory. Tensor cores 56% busy, exponential unit 56%.
 // (Steps of 64 keys with two places for each subtile's scores, so that the next are ready when
 // a row's weights are done, took 571 us: eight waits and twelve commits a tile of keys in the
 // issuing warp.)
@@ -493,8 +495,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             am = max3(am, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
         }
       }
-      // float16 queries, and bfloat16 rows within its range, are exact as they stand; others
-      // are moved by a power of two, taken back from the scores
+      // float16 queries are exact as they stand, bfloat16 rows whose largest is from 2^-10 to 2^15
+      // but for elements below 2^-17, which are taken to 2^-25; other rows are moved by a power
+      // of two, taken back from the scores (and are then exact to 2^-39 of their largest)
       int e = 0;
       if (am > 0.f && am < INFINITY && (am >= 32768.f || am < 0.0009765625f)) e = 14 - ilogbf(am);
       e = min(max(e, -126), 126);
