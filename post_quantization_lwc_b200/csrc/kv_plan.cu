@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(PlanParams p) {
       pos = __ldcg(p.lens_out + req) - end + static_cast<int>(t);
       const uint32_t pg = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page);
       const int id = __ldcg(p.table + static_cast<int64_t>(req) * p.width + pg);
-      slot = id < 0 ? -1
-                    : static_cast<int>(id * p.page + (static_cast<uint32_t>(pos) - pg * p.page));
+      // (an id that no pool has must not come round to a slot of another page)
+      const int64_t at = static_cast<int64_t>(id) * p.page + (static_cast<uint32_t>(pos) - pg * p.page);
+      slot = id < 0 || at > 0x7fffffff ? -1 : static_cast<int>(at);
     }
     p.slots[t] = slot;
     p.positions[t] = pos;
