@@ -569,7 +569,8 @@ omq_status omq_rope_table(int64_t n_pos, int64_t D, double base, float* table,
  * (in place); given other arrays, the call may be repeated with the same result.
  * cu [n_req + 1]: request b's granted tokens are rows cu[b] .. cu[b + 1] - 1 of the step.
  * slots, positions, requests [capacity]: each row's slot, position and request, -1 behind
- * the last row (a slot is -1, too, where its page id is negative or the slot 2^31 or more). Lengths outside 0 .. width * page count as the nearer bound.
+ * the last row (a slot is -1, too, where its page id is negative or the slot 2^31 or more).
+ * Lengths outside 0 .. width * page count as the nearer bound.
  * One launch; n_req up to 65536, width * page < 2^31.
  * ------------------------------------------------------------------------------------ */
 typedef struct {
