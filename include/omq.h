@@ -644,7 +644,7 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * dense, F16 or BF16; lse [T, Hq] float32 (natural log of the softmax's denominator) or NULL.
  * The codes are exact operands and sums, statistics and steps are float32; the weights are
  * rounded to float16 (what is below 2^-39, with many rows 2^-31, of the row's largest is lost).
- * q counts to within 2^-35 of the largest element (below 2^115) of the 8 or 16 rows that are
+ * q counts to within 2^-35 of the largest finite element (below 2^115) of the 8 or 16 rows that are
  * processed together; with many rows float16 exactly, bfloat16 to within 2^-25, or 2^-39 of the
  * row's largest where that is below 2^-10 or from 2^15 on. For a request of more than 64 query
  * rows per kv head (rows = tokens x Hq / Hkv), k and v themselves may be float16 operands (so

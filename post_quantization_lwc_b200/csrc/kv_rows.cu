@@ -398,8 +398,21 @@ __global__ void __launch_bounds__(32 * W, NB == 1 ? 3 : 2)
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (!(am < INFINITY)) {             // of the finite elements, for the sake of the other rows
+      am = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 x = pair(raw[nb][i], f16);
+          am = fmaxf(am, fmaxf(fabsf(x.x) < INFINITY ? fabsf(x.x) : 0.f,
+                               fabsf(x.y) < INFINITY ? fabsf(x.y) : 0.f));
+        }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    }
     int e = 0;
-    if (am > 0.f && am < INFINITY) e = 14 - ilogbf(am);
+    if (am > 0.f) e = 14 - ilogbf(am);
     e = min(max(e, -100), 100);
     const float up = __int_as_float((e + 127) << 23), back = __int_as_float((127 - e) << 23);
     // x = h (acc cq + z sg) + log2 hv: codes and q carry 2^-24 and 2^e
