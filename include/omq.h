@@ -600,7 +600,7 @@ omq_status omq_kv_plan(const omq_kv_plan_args* args, omq_stream_t stream);
  *   q_out = q~ in q_dt, or for abits < 16 its fake-quant with 2^abits - 1 in place of 15
  * A row holding a NaN or an infinity, or whose range or min / h overflows, is stored with
  * h = NaN and reads back as NaN. A row whose |z| is above 2^30 (a constant one beyond 10.7) is
- * stored as c = 0, z = -1 or 1, h = |z h|, which is the same value. RoPE takes pairs
+ * stored as c = 0, z = -2^20 or 2^20, h = |z h| 2^-20, which is the same value. RoPE takes pairs
  * (i, i + D/2) and row positions[t] of the table; no positions (or no table): no rotation.
  * s_a, s_o, delta_o [Hkv, D] or NULL (no transform); query head j shares those of kv head
  * j / (Hq / Hkv).
@@ -649,8 +649,9 @@ omq_status omq_kv_read(const omq_kv_pool* pool, int64_t T, const int32_t* slots,
  * row's largest where that is below 2^-10 or from 2^15 on. For a request of more than 64 query
  * rows per kv head (rows = tokens x Hq / Hkv), k and v themselves may be float16 operands (so
  * |k scale log2 e| and |v| below 65504, and each to within 2^-11 of it and 2^-25): always for
- * more than 512 rows, below by the call's sizes and types. Results are bitwise reproducible on
- * one device. out and lse overlap nothing that is read (out over q: OMQ_ERR_UNSUPPORTED).
+ * more than 512 rows, below by the call's sizes and types; rows that see a key or value beyond are
+ * not finite. Results are bitwise reproducible on one device. out and lse overlap nothing that is
+ * read (out over q: OMQ_ERR_UNSUPPORTED).
  * Workspace: omq_kv_attn_workspace_bytes (may be 0; then it may be NULL), 16-byte aligned, from
  * a query under the device of the call; its contents are nothing before and after. Calls (and
  * graphs) that may run at the same time need one each.

@@ -285,10 +285,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
         }
       }
       // A zero point beyond the stored integer's range has a step of 1e-8, so a row whose values
-      // are all one float32: codes 0, and the same value (0 - z) h with z = -1 or 1.
+      // are all one float32: codes 0, and the same value (0 - z) h with z = -2^20 or 2^20. (A power
+      // of two, so it is exact; so far from the codes that (15 - z) h, by which the attention
+      // tells the rows beyond float16, is the value, too.)
       if (fabsf(g.z) > static_cast<float>(Z_LIMIT)) {
-        zi = g.z < 0.f ? -1 : 1;
-        g.h = fabsf(__fmul_rn(g.z, g.h));
+        zi = g.z < 0.f ? -(1 << 20) : 1 << 20;
+        g.h = fabsf(__fmul_rn(g.z, g.h)) * 9.5367431640625e-07f;
       }
     }
     if (which != 0) {

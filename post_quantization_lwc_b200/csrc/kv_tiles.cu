@@ -835,17 +835,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const uint32_t cells = mask[rs];
         const int left = vis_max - key0 - j * KT;          // keys of the tile that anyone sees
-        // Steps of key t's K or V row. A key that is not there gets zeros. A NaN step is kept
-        // out of V, where it would meet the zero weights of rows that do not see the key, and
-        // put into K instead, whose scores are masked row by row.
+        // Steps of key t's K or V row. A key that is not there gets zeros. A NaN step, or one whose
+        // row has values that float16 rounds to infinity (a row's codes are 0 to 15), is kept out
+        // of V, where it would meet the zero weights of rows that do not see the key, and a NaN put
+        // into K instead, whose scores are masked row by row.
         auto steps = [&](int t, bool k) {
           const uint32_t a = raw + (t >> 4) * C::BYTES + C::KH + 4 * (t & 15);
           float h = 0.f, z = 0.f;
           if (((cells >> (t >> 4)) & 1u) && t < left) {
             const float kh = lds_f(a), vh = lds_f(a + 128);
-            const bool bad = !(kh == kh) || !(vh == vh);
+            const float kz = static_cast<float>(lds_i(a + 64)), vz = static_cast<float>(lds_i(a + 192));
+            const bool bad = !(kh == kh) || !(vh * fmaxf(fabsf(vz), fabsf(15.f - vz)) < 65520.f);
             h = k ? (bad ? NAN : kh * cq) : (bad ? 0.f : vh);
-            z = static_cast<float>(lds_i(a + (k ? 64 : 192)));
+            z = k ? kz : vz;
           }
           return row_steps(h, z);
         };

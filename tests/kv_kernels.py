@@ -14,6 +14,17 @@ from tests import kv_common as kc
 FEW, MOST = 64, 512
 
 
+def encode(x):
+    """kc.encode of the rows of x, and the documented form of a constant row whose zero point is
+    beyond 2^30: c = 0, z = -2^20 or 2^20 and h = |z h| 2^-20 (kc.encode cuts z there)."""
+    c, h, z = kc.encode(x)
+    with np.errstate(all="ignore"):
+        full = -np.rint(x.astype(np.float32).min(-1, keepdims=True) / h)
+        far = np.abs(full) > np.float32(2.0 ** 30)
+        value = np.abs((full * h).astype(np.float32)) * np.float32(2.0 ** -20)
+    return np.where(far, np.float32(0), c), np.where(far, value, h), np.where(far, np.sign(full) * np.float32(2.0 ** 20), z)
+
+
 def tile_kernel(s, b):
     """Whether request b of a Setup runs on the tile kernel, where that does not depend on the
     sizes' estimate: no request has more than 64 rows, or some has more than 512."""

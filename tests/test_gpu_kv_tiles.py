@@ -24,7 +24,7 @@ def omq(cuda_device):
 def refill(s, w, x, b=0):
     """Request b's keys (w = 0) or values (1): the rows x [n, Hkv, D]."""
     pos = np.arange(len(x))
-    s.kv[b][w] = kc.encode(x.astype(np.float32))
+    s.kv[b][w] = kk.encode(x.astype(np.float32))
     s.put(s.pool_np, s.table[b, pos // s.page] * s.page + pos % s.page, w, *s.kv[b][w])
     s.pool.copy_(torch.from_numpy(s.pool_np))
 
