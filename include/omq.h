@@ -571,7 +571,7 @@ omq_status omq_rope_table(int64_t n_pos, int64_t D, double base, float* table,
  * slots, positions, requests [capacity]: each row's slot, position and request, -1 behind
  * the last row (a slot is -1, too, where its page id is negative or the slot 2^31 or more).
  * Lengths outside 0 .. width * page count as the nearer bound.
- * One launch; n_req up to 65536, width * page < 2^31.
+ * One launch; n_req up to 65536, width * page < 2^31, width * min(n_req, 512) < 2^31.
  * ------------------------------------------------------------------------------------ */
 typedef struct {
   const int32_t* lens;         /* [n_req] */

@@ -151,6 +151,8 @@ omq_status omq_kv_plan(const omq_kv_plan_args* a, omq_stream_t stream) {
   if (a->page < 16 || a->page % 16 || a->page > kMaxPage) return OMQ_ERR_SHAPE;
   if (a->width < 1 || a->width >= (int64_t{1} << 31) / a->page) return OMQ_ERR_SHAPE;
   if (a->n_pages < 1 || a->n_pages > (int64_t{1} << 31) / a->page - 1) return OMQ_ERR_SHAPE;
+  // the pages of a chunk of the kernel's 512 requests are counted in 32 bits
+  if (a->width * (a->n_req < 512 ? a->n_req : 512) >= (int64_t{1} << 31)) return OMQ_ERR_SHAPE;
   kv::PlanParams p{a->lens, a->new_tokens, static_cast<int>(a->n_req), a->table,
                    static_cast<int>(a->width), static_cast<int>(a->page), a->free_pages,
                    static_cast<int>(a->n_pages), a->n_free, a->lens_out, a->n_free_out, a->cu,
