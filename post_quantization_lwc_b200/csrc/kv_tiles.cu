@@ -30,9 +30,9 @@
 //   8, 9      expand K; 10, 11 expand V
 //   12        MMA issue (leader CTA); TMEM allocation
 //   13        bulk copies of the raw cells
-// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 505 us (1.09 PFLOP/s) in a burst at
-// 1965 MHz and 567 under load at the power limit (1762 MHz), three chunks of up to 1000 behind
-// contexts of up to 16411 527 us (0.97) and 558 (1867 MHz); 32 heads, 2048 tokens 65 us (0.53: 4 to
+// Measured, 8 x 4 heads of 128: a prompt of 8192 tokens 507 us (1.08 PFLOP/s) in a burst at
+// 1965 MHz and 568 under load at the power limit (1760 MHz), three chunks of up to 1000 behind
+// contexts of up to 16411 533 us (0.96) and 560 (1860 MHz); 32 heads, 2048 tokens 65 us (0.53: 4 to
 // 16 tiles of keys do not hide a pair's first 7 us). A step of 128 keys takes 3550 cycles against
 // 2048 of products and another 2048 of exponentials (256 rows x 128 keys a CTA, 16 a clock); the
 // two meet only partly, a row's chain being read S, maximum, exponentials, write P with no more
