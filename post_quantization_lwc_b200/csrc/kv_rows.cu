@@ -28,9 +28,9 @@
 // through distributed shared memory, one cut otherwise leaves float32 partials in the workspace,
 // which a second kernel joins; in the blocks' order either way.
 //
-// Measured: 64 decoding requests of up to 8192 tokens, 8 x 4 heads of 128: 79 us (4.1 TB/s), one
-// of 131072 38 us (4.0 TB/s), 33 of up to 4001 with 5 drafted tokens, 4 x 2 heads of 64: 21 us, one
-// of 2049, 32 heads 10.5 us. Neither DRAM (49%) nor issue (52%) is full: the registers (168 a
+// Measured: 64 decoding requests of up to 8192 tokens, 8 x 4 heads of 128: 80 us (4.0 TB/s), one
+// of 131072 38 us (4.0 TB/s), 33 of up to 4001 with 5 drafted tokens, 4 x 2 heads of 64: 22 us, one
+// of 2049, 32 heads 10.7 us. Neither DRAM (49%) nor issue (52%) is full: the registers (168 a
 // thread) leave 12 warps an SM, each of which waits on its own chain of scores, weights and
 // products; of the two, loads alone took 70 us and arithmetic alone 84 of then 92.
 #include "kv_internal.cuh"
